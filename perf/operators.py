@@ -494,7 +494,9 @@ def exact(case, seed):
         out = [s["k_pool"].double(), s["v_pool"].double()]
         for x, y, scale in zip(out, (rotated(s["k_new"]), s["v_new"].double()), (s["k_scale"], s["v_scale"])):
             page = (s["slots"] // P).long()
-            x[page, :, (s["slots"] % P).long()] = y / scale.double()[page][..., None] if case["fp8"] else y
+            if case["fp8"]:
+                y = (y / scale.double()[page][..., None]).clamp(-448, 448)      # E4M3 saturates
+            x[page, :, (s["slots"] % P).long()] = y
         return [rotated(s["q"])] + out
     if case["op"] == "commit":
         k, v = values("k_pool"), values("v_pool")
@@ -505,7 +507,8 @@ def exact(case, seed):
         if move:
             p0, a0, p1, a1 = torch.tensor(move, device=DEV).T
             for x, y, scale in zip(out, (k, v), (s["k_scale"], s["v_scale"])):
-                x[p1, :, a1] = y[p0, :, a0] / scale.double()[p1][..., None] if case["fp8"] else y[p0, :, a0]
+                z = y[p0, :, a0]
+                x[p1, :, a1] = (z / scale.double()[p1][..., None]).clamp(-448, 448) if case["fp8"] else z
         return out + [None]
     out = torch.zeros(s["q"].shape, dtype=torch.float64, device=DEV)
     G = case["Hq"] // case["Hkv"]
