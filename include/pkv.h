@@ -63,6 +63,11 @@
  *       host page allocator of pkv_pages.h;
  *   pkv_decode_attn_noalloc                          the attention without a
  *       context (no allocation);
+ *   pkv_slot_map, pkv_rope_append_axes, pkv_decode_attn_tree, pkv_tree_commit
+ *       the step over trees of drafted tokens and over several position axes:
+ *       pages, slots and positions planned on the device, rotation and append
+ *       at given positions and slots, attention under a tree mask, and the
+ *       accepted path moved into place;
  *   pkv_set_workers, pkv_set_tail_chunks, pkv_set_qkv_split, pkv_set_prefill_rows,
  *   pkv_qkv_launch_shape, pkv_workspace_bytes        tuning and inspection.
  *
@@ -70,7 +75,9 @@
  * and launch nothing.  A failed launch returns PKV_ERR_CUDA.  Range errors
  * found on the device (a page id outside [0, num_pages), or L_b + 1 larger
  * than bt_stride * P) skip the affected request or tile and set a sticky
- * device error word, which pkv_check_device_error reads; no call traps.
+ * device error word, which pkv_check_device_error reads; no call traps.  The
+ * four calls of the tree step also want the context's device to be current
+ * (PKV_ERR_INVALID_ARG otherwise).
  * C++ exceptions never cross this ABI.
  */
 #ifndef PKV_H
@@ -285,6 +292,131 @@ pkv_status pkv_table_sync(const int32_t* upload, int n_changes, int batch, int m
                           int page_size, int32_t* table, int32_t* bt_out, int32_t* lens_out,
                           cudaStream_t stream);
 
+/* Plan of a step on the device, from lengths that only the GPU knows (after a
+ * speculative step the accepted counts are device data, and reading them back
+ * would stall the loop): pages for the new tokens, a slot and a position for
+ * each, and the masks of drafted trees ("TensorRT-LLM Guide: High-Throughput
+ * GPU Inference Engine", section "2. Paged KV Cache & Memory
+ * Virtualization": pages allocated on demand, a table maps logical positions
+ * to physical blocks; "Scaling TensorRT-LLM: Kernel Fusion and Inflight
+ * Batching in Production", section "3. Speculative Decoding for Tail
+ * Latency").  Request b holds L_b = seq_lens[b] cached tokens in its first
+ * pages_held[b] >= ceil(L_b / P) table entries and gets n_b = new_lens[b] new
+ * tokens, packed in request order (rows cu_q[b] .. cu_q[b + 1] - 1).
+ *
+ *   need_b = max(pages_held[b], ceil((L_b + n_b) / P)); the pages it lacks are
+ *       popped off the free stack in request order: the k-th page taken by
+ *       the call is free_pages[free_count[0] - 1 - k];
+ *   new token i of request b: slot (page of position L_b + i) * P +
+ *       (L_b + i) % P, and position L_b + i; or, with `parents`, L_b + depth,
+ *       where parents[row] is the place in its request of the token's parent
+ *       (smaller than its own place), -1 for a child of the cached prefix
+ *       (depth 0);
+ *   tree_mask[row]: bit j of word w set when drafted token 32 w + j of the
+ *       request is the row's token or one of its ancestors.
+ *
+ *   seq_lens, new_lens, pages_held  int32 [batch];  parents int32 [n_tokens] or NULL
+ *   block_tables  int32 [batch][bt_stride], entries [pages_held, need) written
+ *   pages_out     int32 [batch] receives need_b; may be pages_held
+ *   free_pages    int32 [free_cap]; free_count int32 [1] entries used;
+ *   free_left     int32 [1] receives the entries left; may be free_count
+ *   n_tokens      rows of slots, positions and tree_mask (their capacity)
+ *   cu_q          int32 [batch + 1]
+ *   slots, positions  int32 [n_tokens]; rows behind the last token get -1, so
+ *       that a captured step of a fixed size skips them
+ *   tree_mask     [n_tokens][mask_words] 32-bit words; NULL exactly when
+ *       parents is NULL; rows behind the last token get 0
+ * Apart from the two pairs named, no output may overlap an input.  All
+ * pointers 4-byte aligned.  batch == 0 is a no-op.
+ *
+ * Device-side errors, each sticky in the error word: a request whose pages
+ * the stack cannot cover keeps pages_held, its tokens get slot -1 and no page
+ * is taken for it (PKV_ERR_OOM; requests before it, and later ones that need
+ * no page, are served); a length, count or held value out of range, more
+ * drafted tokens than 32 mask_words, or a parent that is not an earlier token
+ * (slot -1, PKV_ERR_DEVICE_BOUNDS); a table or stack entry that is no page
+ * (the slots in it -1); more tokens than n_tokens (the surplus dropped, cu_q
+ * clipped). */
+pkv_status pkv_slot_map(pkv_ctx* ctx, const int32_t* seq_lens, const int32_t* new_lens, const int32_t* parents,
+                        int batch, int32_t* block_tables, int bt_stride, const int32_t* pages_held,
+                        int32_t* pages_out, const int32_t* free_pages, int free_cap, const int32_t* free_count,
+                        int32_t* free_left, int n_tokens, int mask_words, int32_t* cu_q, int32_t* slots,
+                        int32_t* positions, uint32_t* tree_mask, cudaStream_t stream);
+
+/* Step part 1 at given positions and slots, with several position axes (the
+ * time, height and width of image and video tokens; one axis for the drafted
+ * tokens of a tree): RoPE and the append of pkv_rope_append, where pair i of
+ * token t turns by the angle positions[axis(i)][t] * rope_base^(-2i/d).
+ *   sections     host int [n_axes] (1 .. 4 axes), pairs per axis, each >= 0,
+ *                their sum d / 2
+ *   interleaved  0: the pairs of an axis are consecutive (the first
+ *                sections[0] pairs turn by axis 0, and so on).  1: pair i
+ *                turns by axis a = i % n_axes while i < n_axes * sections[a],
+ *                else by axis 0; every axis a > 0 then has its sections[a]
+ *                pairs below d / 2 (n_axes * (sections[a] - 1) + a < d / 2,
+ *                PKV_ERR_INVALID_ARG otherwise)
+ *   q [n_tokens][Hq][d], k_new / v_new [n_tokens][Hkv][d] bf16
+ *   q_out        [n_tokens][Hq][d] rotated q; q itself for in place, else no
+ *                overlap with an input
+ *   positions    int32 [n_axes][n_tokens], any value
+ *   slots        int32 [n_tokens]: page * P + place in the page, as
+ *                pkv_slot_map writes them; -1 skips the token (q_out, too, is
+ *                left as it was).  A slot outside the pools sets the error
+ *                word and is skipped; two tokens of one slot race for it.
+ * Rotation in fp32 from angles reduced in fp64 (far positions keep their
+ * fraction), rounded once to the storage type; E4M3 pools as for
+ * pkv_rope_append.  n_tokens == 0 is a no-op. */
+pkv_status pkv_rope_append_axes(pkv_ctx* ctx, const void* q, const void* k_new, const void* v_new, int n_tokens,
+                                const int32_t* positions, int n_axes, const int* sections, int interleaved,
+                                const int32_t* slots, void* q_out, void* k_pool, void* v_pool,
+                                const float* k_scale, const float* v_scale, cudaStream_t stream);
+
+/* Step part 2 over trees of drafted tokens: the verification of speculative
+ * decoding where a draft proposes several continuations at once.  The new
+ * tokens are packed (cu_q as for pkv_decode_attn_varlen, T_b of request b);
+ * new token i of request b sits in slot L_b + i of its pages (L_b =
+ * seq_lens[b]; its rotary position is its own affair) and attends the cached
+ * tokens 0 .. L_b - 1 and those new tokens j of its request whose bit is set
+ * in its mask row: bit j % 32 of tree_mask[row][j / 32] (itself included only
+ * if its own bit is set).  A row that sees nothing (L_b = 0 and no bit) is
+ * zero.  Bits at and past T_b are ignored.
+ *   q, out     [n_tokens][Hq][d] bf16; rows outside every request are left
+ *              as they were.  q and out may not overlap.
+ *   tree_mask  [n_tokens][mask_words] 32-bit words, T_b <= 32 mask_words
+ * bf16 or E4M3 pools (scales as for pkv_decode_attn).  The cache is read once
+ * for every 2 * (128 / G) new tokens of a request.  The work is split over
+ * the SMs along the cache, and partial results are merged by log-sum-exp in a
+ * fixed order: results repeat bit for bit.  A request with lengths out of
+ * range, or more than 32 mask_words new tokens, gets zeros and sets the error
+ * word; keys in a page out of range are left out and set it; a request whose
+ * cu_q entries are not 0 <= cu_q[b] <= cu_q[b + 1] <= n_tokens is skipped and
+ * sets it.  batch == 0 or n_tokens == 0 is a no-op. */
+pkv_status pkv_decode_attn_tree(pkv_ctx* ctx, const void* q, const void* k_pool, const void* v_pool,
+                                const float* k_scale, const float* v_scale, const int32_t* block_tables,
+                                int bt_stride, const int32_t* seq_lens, const int32_t* cu_q,
+                                const uint32_t* tree_mask, int mask_words, int batch, int n_tokens, void* out,
+                                cudaStream_t stream);
+
+/* The accepted path of each request's tree moved to the front of its new
+ * tokens' slots: K and V of slot L_b + path[b][j] go to slot L_b + j, j <
+ * path_lens[b], and lens_out[b] = L_b + path_lens[b].
+ *   path       int32 [batch][path_stride], strictly increasing in each row,
+ *              from 0 up (a path from the prefix down a tree whose parents
+ *              come before their children)
+ *   path_lens  int32 [batch], 0 .. path_stride
+ *   lens_out   int32 [batch]; may be seq_lens
+ * bf16 rows and E4M3 rows that stay on scales of the same value are copied
+ * bit for bit; E4M3 rows that cross to a page of another scale are stored
+ * again as E4M3_RNE_satfinite(fl32(fl32(code * old scale) / new scale)).  The
+ * slots behind the accepted ones keep their contents.  A request with a bad
+ * length, path or page is left alone (lens_out = seq_lens) and sets the error
+ * word.  Requests must not share the pages of their new tokens.  batch == 0
+ * is a no-op. */
+pkv_status pkv_tree_commit(pkv_ctx* ctx, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,
+                           const int32_t* block_tables, int bt_stride, const int32_t* seq_lens,
+                           const int32_t* path, int path_stride, const int32_t* path_lens, int batch,
+                           int32_t* lens_out, cudaStream_t stream);
+
 /* Layouts of the QKV weight for pkv_qkv_rope_append. */
 enum { PKV_W_ROWS = 0, PKV_W_TILED = 1 };
 
@@ -305,9 +437,10 @@ pkv_status pkv_destroy(pkv_ctx* ctx);
 const char* pkv_status_str(pkv_status s);
 
 /* Synchronises `stream`, reads and clears the context's device error word.
- * Returns PKV_OK, PKV_ERR_DEVICE_BOUNDS or PKV_ERR_DEVICE_TIMEOUT; if
- * `bits` is not NULL it receives the raw word (1: length out of range,
- * 2: page id out of range, 4: wait timed out). */
+ * Returns PKV_OK, PKV_ERR_DEVICE_TIMEOUT, PKV_ERR_DEVICE_BOUNDS or PKV_ERR_OOM
+ * (in that order of precedence); if `bits` is not NULL it receives the raw
+ * word (1: length out of range, 2: page id out of range, 4: wait timed out,
+ * 8: a parent or path entry out of order, 16: the free pages ran out). */
 pkv_status pkv_check_device_error(pkv_ctx* ctx, cudaStream_t stream, int* bits);
 
 /* Caps the number of warp workers pkv_decode_attn splits the token ranges

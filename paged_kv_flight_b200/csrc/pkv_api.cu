@@ -13,56 +13,14 @@
 
 #include <cudaTypedefs.h>
 
-#include "pkv_internal.h"
-
-struct pkv_ctx {
-    pkv_config cfg;
-    int device;
-    int num_sms;
-    int G;
-    pkv::AttnLaunch attn;
-    pkv::AttnLaunch attn_tok;     // several new tokens per request
-    int workers;
-    int tail_chunks;      // largest number of dynamic tail chunks per warp range
-    void* ws;             // one allocation, carved below
-    size_t ws_bytes;
-    int* d_err;
-    int* d_claim;         // chunk counter of the attention's dynamic tail
-    double* d_theta;      // [head_dim / 2] rope_base^(-2i/d), fp64
-    int* d_meta;
-    int vmax;             // virtual requests a varlen attention call may have (bf16 pools)
-    int4* d_vmap;         // [vmax] the varlen plan
-    int* d_vcount;
-    int prefill_rows;     // varlen requests with G x new tokens >= this go to the prefill-chunk kernel (0: none)
-    int4* d_cmap;         // [vmax] its blocks
-    int* d_ccount;
-    float* d_part_o;
-    float* d_part_ml;
-    const void* tm_k_ptr;
-    const void* tm_v_ptr;
-    CUtensorMap tmk, tmv;
-    // 16-row boxes for the several-new-tokens path where the one-token maps
-    // use 32-row ones (E4M3 pools with pages of 32 tokens or more)
-    const void* t16_k_ptr;
-    const void* t16_v_ptr;
-    CUtensorMap t16k, t16v;
-    // page-high boxes (P rows) for the prefill-chunk kernel (bf16 pools)
-    const void* tp_k_ptr;
-    const void* tp_v_ptr;
-    CUtensorMap tpk, tpv;
-    const void* tm_w_ptr;        // QKV weight and input maps of pkv_qkv_rope_append
-    int tm_w_hidden, tm_w_layout;
-    int qkv_split;               // 0: automatic
-    int plan_key[6];             // (x_rows, D, heads, tiles, hidden, forced split) of the cached plan
-    pkv::QkvPlan plan;
-    const void* tm_x_ptr;
-    int tm_x_hidden, tm_x_rows;
-    CUtensorMap tmw, tmx;
-};
+#include "pkv_ctx.h"
+#include "tree_params.h"
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+using pkv::aligned16;
+using pkv::check_call;
+using pkv::encode_pool_rows;
 
 pkv_status validate_config(const pkv_config* c)
 {
@@ -80,23 +38,6 @@ pkv_status validate_config(const pkv_config* c)
     if (c->max_batch > pkv::kMaxBatch) return PKV_ERR_UNSUPPORTED;
     // TMA row coordinates are int32
     if ((long long)c->num_pages * c->num_kv_heads * c->page_size >= (1LL << 31)) return PKV_ERR_UNSUPPORTED;
-    return PKV_OK;
-}
-
-pkv_status check_call(const pkv_ctx* ctx, int batch, int bt_stride, const void* k_pool,
-                      const void* v_pool, const float* k_scale, const float* v_scale,
-                      const int32_t* block_tables, const int32_t* seq_lens)
-{
-    if (!ctx) return PKV_ERR_INVALID_ARG;
-    if (batch < 0 || batch > ctx->cfg.max_batch) return PKV_ERR_INVALID_ARG;
-    if (batch == 0) return PKV_OK;
-    if (bt_stride <= 0 || bt_stride > ctx->cfg.max_blocks_per_seq) return PKV_ERR_INVALID_ARG;
-    if (!k_pool || !v_pool || !block_tables || !seq_lens) return PKV_ERR_INVALID_ARG;
-    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(block_tables) || !aligned16(seq_lens))
-        return PKV_ERR_INVALID_ARG;
-    if (ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3) {
-        if (!k_scale || !v_scale || !aligned16(k_scale) || !aligned16(v_scale)) return PKV_ERR_INVALID_ARG;
-    }
     return PKV_OK;
 }
 
@@ -118,32 +59,10 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
 // elements; box = one attention tile of rows (16, or 32 for E4M3 pools with
 // pages of at least 32 tokens) x (128 or 64 bytes), swizzled to match the
 // kernel's shared-memory addressing.
-bool encode_pool_rows(const pkv_ctx* ctx, const void* pool, int box_rows, CUtensorMap* map);
-
 bool encode_pool(const pkv_ctx* ctx, const void* pool, CUtensorMap* map)
 {
     const bool fp8 = ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3;
     return encode_pool_rows(ctx, pool, pkv::attn_tile(fp8, ctx->cfg.page_size), map);
-}
-
-bool encode_pool_rows(const pkv_ctx* ctx, const void* pool, int box_rows, CUtensorMap* map)
-{
-    auto fn = encode_fn();
-    if (!fn) return false;
-    const bool fp8 = ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3;
-    const int elem = fp8 ? 1 : 2;
-    const int rowb = ctx->cfg.head_dim * elem;
-    const int boxb = rowb > 128 ? 128 : rowb;
-    cuuint64_t dims[2] = {(cuuint64_t)ctx->cfg.head_dim,
-                          (cuuint64_t)ctx->cfg.num_pages * ctx->cfg.num_kv_heads * ctx->cfg.page_size};
-    cuuint64_t strides[1] = {(cuuint64_t)rowb};
-    cuuint32_t box[2] = {(cuuint32_t)(boxb / elem), (cuuint32_t)box_rows};
-    cuuint32_t estr[2] = {1, 1};
-    CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-                    const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                    boxb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS;
 }
 
 // 2-D view of a row-major bf16 matrix [rows][cols] for the projection's TMA
@@ -178,6 +97,47 @@ bool qkv_plan_for(pkv_ctx* ctx, int batch, int hidden)
 
 }  // namespace
 
+namespace pkv {
+
+pkv_status check_call(const pkv_ctx* ctx, int batch, int bt_stride, const void* k_pool,
+                      const void* v_pool, const float* k_scale, const float* v_scale,
+                      const int32_t* block_tables, const int32_t* seq_lens)
+{
+    if (!ctx) return PKV_ERR_INVALID_ARG;
+    if (batch < 0 || batch > ctx->cfg.max_batch) return PKV_ERR_INVALID_ARG;
+    if (batch == 0) return PKV_OK;
+    if (bt_stride <= 0 || bt_stride > ctx->cfg.max_blocks_per_seq) return PKV_ERR_INVALID_ARG;
+    if (!k_pool || !v_pool || !block_tables || !seq_lens) return PKV_ERR_INVALID_ARG;
+    if (!aligned16(k_pool) || !aligned16(v_pool) || !aligned16(block_tables) || !aligned16(seq_lens))
+        return PKV_ERR_INVALID_ARG;
+    if (ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3) {
+        if (!k_scale || !v_scale || !aligned16(k_scale) || !aligned16(v_scale)) return PKV_ERR_INVALID_ARG;
+    }
+    return PKV_OK;
+}
+
+bool encode_pool_rows(const pkv_ctx* ctx, const void* pool, int box_rows, CUtensorMap* map)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const bool fp8 = ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3;
+    const int elem = fp8 ? 1 : 2;
+    const int rowb = ctx->cfg.head_dim * elem;
+    const int boxb = rowb > 128 ? 128 : rowb;
+    cuuint64_t dims[2] = {(cuuint64_t)ctx->cfg.head_dim,
+                          (cuuint64_t)ctx->cfg.num_pages * ctx->cfg.num_kv_heads * ctx->cfg.page_size};
+    cuuint64_t strides[1] = {(cuuint64_t)rowb};
+    cuuint32_t box[2] = {(cuuint32_t)(boxb / elem), (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    CUresult r = fn(map, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                    const_cast<void*>(pool), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    boxb == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+}  // namespace pkv
+
 extern "C" {
 
 pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
@@ -208,12 +168,13 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
         free(ctx);
         return PKV_ERR_CUDA;
     }
-    if (pkv::qkv_prepare() != cudaSuccess || pkv::chunk_attn_prepare(cfg->head_dim) != cudaSuccess) {
+    if (pkv::qkv_prepare() != cudaSuccess || pkv::chunk_attn_prepare(cfg->head_dim) != cudaSuccess ||
+        pkv::slot_map_prepare() != cudaSuccess) {
         free(ctx);
         return PKV_ERR_CUDA;
     }
 
-    // [error word, chunk counter | split geometry | partial rows | partial (m, l)];
+    // [error word, chunk counter, slot-map counter | split geometry | partial rows | partial (m, l)];
     // two partial slots per unit of the split: G rows each for one new token
     // per request (up to kMaxTailChunks + 1 units per warp), up to
     // kMaxTokenRows rows for several (one unit per warp)
@@ -234,6 +195,7 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
     uint8_t* base = static_cast<uint8_t*>(ctx->ws);
     ctx->d_err = reinterpret_cast<int*>(base);
     ctx->d_claim = reinterpret_cast<int*>(base + 128);
+    ctx->d_done = reinterpret_cast<unsigned*>(base + 192);
     ctx->tail_chunks = pkv::kDefaultTailChunks;
     ctx->d_meta = reinterpret_cast<int*>(base + b_err);
     ctx->d_part_o = reinterpret_cast<float*>(base + b_err + b_cnt);
@@ -720,7 +682,8 @@ pkv_status pkv_check_device_error(pkv_ctx* ctx, cudaStream_t stream, int* bits)
     if (word && cudaMemset(ctx->d_err, 0, sizeof(int)) != cudaSuccess) return PKV_ERR_CUDA;
     if (bits) *bits = word;
     if (word & pkv::kErrTimeout) return PKV_ERR_DEVICE_TIMEOUT;
-    if (word & (pkv::kErrLength | pkv::kErrPage)) return PKV_ERR_DEVICE_BOUNDS;
+    if (word & (pkv::kErrLength | pkv::kErrPage | pkv::kErrOrder)) return PKV_ERR_DEVICE_BOUNDS;
+    if (word & pkv::kErrNoPages) return PKV_ERR_OOM;
     return PKV_OK;
 }
 

@@ -12,7 +12,7 @@
 namespace pkv {
 
 // Device error bits (sticky word in the context workspace).
-enum : int { kErrLength = 1, kErrPage = 2, kErrTimeout = 4 };
+enum : int { kErrLength = 1, kErrPage = 2, kErrTimeout = 4, kErrOrder = 8, kErrNoPages = 16 };
 
 // Warps per attention CTA (one CTA per SM) and the deepest per-warp TMA
 // ring; both can be overridden at build time for tuning sweeps.

@@ -1,0 +1,84 @@
+// tree_params.h -- parameters and launchers of the tree step's kernels
+// (slot_map.cu, rope_axes.cu, tree_attn.cu, tree_commit.cu), shared with its
+// host side (tree_api.cu).  Not part of the ABI.
+#pragma once
+
+#include "pkv_internal.h"
+
+namespace pkv {
+
+struct SlotMapParams {
+    const int32_t* seq_lens;
+    const int32_t* new_lens;
+    const int32_t* parents;       // null: a chain
+    int32_t* block_tables;
+    const int32_t* pages_held;
+    int32_t* pages_out;           // may be pages_held
+    const int32_t* free_pages;
+    const int32_t* free_count;
+    int32_t* free_left;           // may be free_count
+    int32_t* cu_q;
+    int32_t* slots;
+    int32_t* positions;
+    uint32_t* tree_mask;
+    unsigned* done;               // CTAs that have finished reading; wraps to 0 at the end of a launch
+    int* err;
+    int batch, bt_stride, free_cap, n_tokens, mask_words, P, num_pages;
+};
+cudaError_t slot_map_prepare();
+cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream);
+
+constexpr int kMaxAxes = 4;
+
+struct RopeAxesParams {
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k_new;
+    const __nv_bfloat16* v_new;
+    const int32_t* positions;     // [n_axes][n_tokens]
+    const int32_t* slots;
+    __nv_bfloat16* q_out;         // may be q
+    void* k_pool;
+    void* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    const double* theta;          // [D / 2] rope_base^(-2i/D) in fp64, from the context
+    int* err;
+    int n_tokens, Hq, Hkv, P, num_pages;
+    int n_axes, interleaved;
+    int bound[kMaxAxes];          // consecutive: the first pair past axis a; interleaved: n_axes * sections[a]
+};
+cudaError_t launch_rope_axes(const RopeAxesParams& p, int head_dim, bool fp8, cudaStream_t stream);
+
+struct TreeAttnParams {
+    const __nv_bfloat16* q;
+    __nv_bfloat16* out;
+    const void* k_pool;
+    const void* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* cu_q;
+    const uint32_t* tree_mask;
+    int* err;
+    float scale_log2;             // log2(e) / sqrt(d)
+    int batch, bt_stride, Hq, Hkv, G, P, num_pages, mask_words, n_tokens;
+};
+cudaError_t launch_tree_attn(const TreeAttnParams& p, int head_dim, bool fp8, cudaStream_t stream);
+
+struct TreeCommitParams {
+    void* k_pool;
+    void* v_pool;
+    const float* k_scale;
+    const float* v_scale;
+    const int32_t* block_tables;
+    const int32_t* seq_lens;
+    const int32_t* path;
+    const int32_t* path_lens;
+    int32_t* lens_out;            // may be seq_lens
+    int* err;
+    int batch, bt_stride, path_stride, Hkv, P, num_pages;
+};
+cudaError_t launch_tree_commit(const TreeCommitParams& p, int head_dim, bool fp8, cudaStream_t stream);
+
+}  // namespace pkv

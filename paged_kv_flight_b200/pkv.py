@@ -49,7 +49,8 @@ EXPORTS = ("pkv_create", "pkv_rope_append", "pkv_decode_attn", "pkv_destroy", "p
            "pkv_pages_release", "pkv_pages_block_table", "pkv_pages_seq_lens", "pkv_pages_active",
            "pkv_pages_refcount", "pkv_pages_free_count", "pkv_pages_take_changes", "pkv_qkv_rope_append",
            "pkv_qkv_pack_weight", "pkv_set_qkv_split", "pkv_qkv_launch_shape",
-           "pkv_table_sync", "pkv_rope_append_varlen", "pkv_decode_attn_varlen", "pkv_decode_step")
+           "pkv_table_sync", "pkv_rope_append_varlen", "pkv_decode_attn_varlen", "pkv_decode_step",
+           "pkv_slot_map", "pkv_rope_append_axes", "pkv_decode_attn_tree", "pkv_tree_commit")
 
 
 class pkv_config(C.Structure):
@@ -119,6 +120,15 @@ lib.pkv_decode_attn_noalloc.argtypes = [C.POINTER(pkv_config), _V, _V, _V, _V, _
 lib.pkv_decode_attn_noalloc.restype = C.c_int
 lib.pkv_decode_step.argtypes = [_V, _V, _V, _V, _V, _V, _V, _V, _V, C.c_int, _V, C.c_int, C.c_int, _V, _V]
 lib.pkv_decode_step.restype = C.c_int
+_I = C.c_int
+lib.pkv_slot_map.argtypes = [_V, _V, _V, _V, _I, _V, _I, _V, _V, _V, _I, _V, _V, _I, _I, _V, _V, _V, _V, _V]
+lib.pkv_slot_map.restype = _I
+lib.pkv_rope_append_axes.argtypes = [_V, _V, _V, _V, _I, _V, _I, C.POINTER(_I), _I, _V, _V, _V, _V, _V, _V, _V]
+lib.pkv_rope_append_axes.restype = _I
+lib.pkv_decode_attn_tree.argtypes = [_V, _V, _V, _V, _V, _V, _V, _I, _V, _V, _V, _I, _I, _I, _V, _V]
+lib.pkv_decode_attn_tree.restype = _I
+lib.pkv_tree_commit.argtypes = [_V, _V, _V, _V, _V, _V, _I, _V, _V, _I, _V, _I, _V, _V]
+lib.pkv_tree_commit.restype = _I
 
 
 class PkvError(RuntimeError):
@@ -480,3 +490,92 @@ def pkv_qkv_rope_append(ctx, x, w_qkv, q_out, k_pool, v_pool, k_scale, v_scale, 
                                  _ptr(block_tables, _I32, "block_tables"), int(bt_stride),
                                  _ptr(seq_lens, _I32, "seq_lens"), int(batch), _stream(stream))
     return _done(st, "pkv_qkv_rope_append", check)
+
+
+def _rows(x, shape, name):
+    """Checks the shape of a tensor argument (None in `shape`: any size); raw
+    pointers pass."""
+    if isinstance(x, torch.Tensor) and (x.dim() != len(shape) or
+                                        any(n is not None and n != m for n, m in zip(shape, x.shape))):
+        raise ValueError(f"{name}: expected shape {tuple('any' if n is None else n for n in shape)}, "
+                         f"got {tuple(x.shape)}")
+
+
+def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, free_count, cu_q, slots, positions,
+                 pages_out, free_left, parents=None, tree_mask=None, stream=None, check: bool = True) -> int:
+    """Pages for every request's new tokens (off the stack free_pages[:
+    free_count], into block_tables), their first rows cu_q [batch + 1], slots
+    and positions [capacity] (-1 behind the last token); with parents
+    [capacity] also the ancestor masks tree_mask [capacity, words].  pages_out
+    [batch] may be pages_held and free_left [1] may be free_count (in place)."""
+    batch, stride = int(block_tables.shape[0]), int(block_tables.shape[1])
+    n_tokens = int(slots.shape[0])
+    for x, shape, name in ((seq_lens, (batch,), "seq_lens"), (new_lens, (batch,), "new_lens"),
+                           (pages_held, (batch,), "pages_held"), (pages_out, (batch,), "pages_out"),
+                           (cu_q, (batch + 1,), "cu_q"), (positions, (n_tokens,), "positions"),
+                           (free_pages, (None,), "free_pages"), (free_count, (1,), "free_count"),
+                           (free_left, (1,), "free_left"), (parents, (n_tokens,), "parents"),
+                           (tree_mask, (n_tokens, None), "tree_mask")):
+        _rows(x, shape, name)
+    st = lib.pkv_slot_map(ctx, _ptr(seq_lens, _I32, "seq_lens"), _ptr(new_lens, _I32, "new_lens"),
+                          _ptr(parents, _I32, "parents"), batch, _ptr(block_tables, _I32, "block_tables"), stride,
+                          _ptr(pages_held, _I32, "pages_held"), _ptr(pages_out, _I32, "pages_out"),
+                          _ptr(free_pages, _I32, "free_pages"), int(free_pages.shape[0]),
+                          _ptr(free_count, _I32, "free_count"), _ptr(free_left, _I32, "free_left"), n_tokens,
+                          0 if tree_mask is None else int(tree_mask.shape[1]), _ptr(cu_q, _I32, "cu_q"),
+                          _ptr(slots, _I32, "slots"), _ptr(positions, _I32, "positions"),
+                          _ptr(tree_mask, _I32, "tree_mask"), _stream(stream))
+    return _done(st, "pkv_slot_map", check)
+
+
+def pkv_rope_append_axes(ctx, q, k_new, v_new, positions, sections, slots, q_out, k_pool, v_pool, k_scale, v_scale,
+                         interleaved: bool = False, stream=None, check: bool = True) -> int:
+    """q / q_out [n_tokens, Hq, d] (q_out may be q), k_new / v_new [n_tokens,
+    Hkv, d], positions [axes, n_tokens], slots [n_tokens] (page * page_size +
+    place, -1 skips the token); sections: pairs of each axis, d / 2 in all."""
+    n, d = int(q.shape[0]), int(q.shape[2])
+    _rows(k_new, (n, None, d), "k_new")
+    _rows(v_new, tuple(k_new.shape), "v_new")
+    _rows(positions, (len(sections), n), "positions")
+    _rows(slots, (n,), "slots")
+    _rows(q_out, tuple(q.shape), "q_out")
+    sec = (_I * len(sections))(*(int(x) for x in sections))
+    st = lib.pkv_rope_append_axes(ctx, _ptr(q, _ACT, "q"), _ptr(k_new, _ACT, "k_new"), _ptr(v_new, _ACT, "v_new"), n,
+                                  _ptr(positions, _I32, "positions"), len(sections), sec, int(bool(interleaved)),
+                                  _ptr(slots, _I32, "slots"), _ptr(q_out, _ACT, "q_out"),
+                                  *_kv(k_pool, v_pool, k_scale, v_scale), _stream(stream))
+    return _done(st, "pkv_rope_append_axes", check)
+
+
+def pkv_decode_attn_tree(ctx, q, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, cu_q, tree_mask, out,
+                         stream=None, check: bool = True) -> int:
+    """q / out [n_tokens, Hq, d]; cu_q [batch + 1] int32; tree_mask [n_tokens,
+    words] int32: bit j % 32 of word j / 32 lets the row see new token j of
+    its request (the cached tokens are always seen)."""
+    batch, n = int(seq_lens.shape[0]), int(q.shape[0])
+    _rows(block_tables, (batch, None), "block_tables")
+    _rows(cu_q, (batch + 1,), "cu_q")
+    _rows(tree_mask, (n, None), "tree_mask")
+    _rows(out, tuple(q.shape), "out")
+    st = lib.pkv_decode_attn_tree(ctx, _ptr(q, _ACT, "q"), *_kv(k_pool, v_pool, k_scale, v_scale),
+                                  _ptr(block_tables, _I32, "block_tables"), int(block_tables.shape[1]),
+                                  _ptr(seq_lens, _I32, "seq_lens"), _ptr(cu_q, _I32, "cu_q"),
+                                  _ptr(tree_mask, _I32, "tree_mask"), int(tree_mask.shape[1]), batch, n,
+                                  _ptr(out, _ACT, "out"), _stream(stream))
+    return _done(st, "pkv_decode_attn_tree", check)
+
+
+def pkv_tree_commit(ctx, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens, path, path_lens, lens_out,
+                    stream=None, check: bool = True) -> int:
+    """path [batch, depth] int32, its first path_lens[b] entries the accepted
+    new tokens of request b in rising order; lens_out [batch] may be seq_lens."""
+    batch = int(seq_lens.shape[0])
+    _rows(block_tables, (batch, None), "block_tables")
+    _rows(path, (batch, None), "path")
+    _rows(path_lens, (batch,), "path_lens")
+    _rows(lens_out, (batch,), "lens_out")
+    st = lib.pkv_tree_commit(ctx, *_kv(k_pool, v_pool, k_scale, v_scale), _ptr(block_tables, _I32, "block_tables"),
+                             int(block_tables.shape[1]), _ptr(seq_lens, _I32, "seq_lens"), _ptr(path, _I32, "path"),
+                             int(path.shape[1]), _ptr(path_lens, _I32, "path_lens"), batch,
+                             _ptr(lens_out, _I32, "lens_out"), _stream(stream))
+    return _done(st, "pkv_tree_commit", check)
