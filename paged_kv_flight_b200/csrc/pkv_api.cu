@@ -136,6 +136,33 @@ bool encode_pool_rows(const pkv_ctx* ctx, const void* pool, int box_rows, CUtens
     return r == CUDA_SUCCESS;
 }
 
+bool page_maps(pkv_ctx* ctx, const void* k_pool, const void* v_pool)
+{
+    if (ctx->tp_k_ptr != k_pool) {
+        if (!encode_pool_rows(ctx, k_pool, ctx->cfg.page_size, &ctx->tpk)) return false;
+        ctx->tp_k_ptr = k_pool;
+    }
+    if (ctx->tp_v_ptr != v_pool) {
+        if (!encode_pool_rows(ctx, v_pool, ctx->cfg.page_size, &ctx->tpv)) return false;
+        ctx->tp_v_ptr = v_pool;
+    }
+    return true;
+}
+
+bool encode_q_rows(const pkv_ctx* ctx, const void* q, int n_tokens, int tokens, CUtensorMap* map)
+{
+    auto fn = encode_fn();
+    if (!fn) return false;
+    const cuuint64_t row = (cuuint64_t)ctx->cfg.head_dim * 2;
+    cuuint64_t dims[3] = {(cuuint64_t)ctx->cfg.head_dim, (cuuint64_t)ctx->cfg.num_q_heads, (cuuint64_t)n_tokens};
+    cuuint64_t strides[2] = {row, row * (cuuint64_t)ctx->cfg.num_q_heads};
+    cuuint32_t box[3] = {64, (cuuint32_t)ctx->G, (cuuint32_t)tokens};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace pkv
 
 extern "C" {
@@ -169,7 +196,7 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
         return PKV_ERR_CUDA;
     }
     if (pkv::qkv_prepare() != cudaSuccess || pkv::chunk_attn_prepare(cfg->head_dim) != cudaSuccess ||
-        pkv::slot_map_prepare() != cudaSuccess) {
+        pkv::slot_map_prepare() != cudaSuccess || pkv::tree_attn_prepare(cfg->head_dim, fp8) != cudaSuccess) {
         free(ctx);
         return PKV_ERR_CUDA;
     }
@@ -186,7 +213,12 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
     const size_t b_pml = 2 * rows_units * 2 * sizeof(float);
     const size_t b_vm = 2 * ((size_t)ctx->vmax * sizeof(int4) + 256);   // varlen plans (virtual, chunk) + counts
     const size_t b_th = ((size_t)cfg->head_dim / 2 * sizeof(double) + 255) & ~(size_t)255;   // RoPE frequencies
-    ctx->ws_bytes = b_err + b_cnt + b_po + b_pml + b_vm + b_th;
+    // the tree attention: two parts of 256 rows per CTA, and where the CTAs start
+    ctx->tree_runs = std::min(ctx->num_sms, pkv::kMaxTreeRuns);
+    const size_t t_rows = 2 * (size_t)ctx->tree_runs * 2 * pkv::kTreeRows;
+    const size_t b_to = t_rows * cfg->head_dim * sizeof(float), b_tml = t_rows * sizeof(float2);
+    const size_t b_tp = ((size_t)(ctx->tree_runs + 1) * sizeof(int4) + 255) & ~(size_t)255;
+    ctx->ws_bytes = b_err + b_cnt + b_po + b_pml + b_vm + b_th + b_to + b_tml + b_tp;
     if (cudaMalloc(&ctx->ws, ctx->ws_bytes) != cudaSuccess) {
         cudaGetLastError();
         free(ctx);
@@ -206,6 +238,9 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
     ctx->d_cmap = reinterpret_cast<int4*>(base + b_err + b_cnt + b_po + b_pml + b_vm / 2 + 256);
     ctx->prefill_rows = pkv::kDefaultPrefillRows;
     ctx->d_theta = reinterpret_cast<double*>(base + b_err + b_cnt + b_po + b_pml + b_vm);
+    ctx->d_tree_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ctx->d_theta) + b_th);
+    ctx->d_tree_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ctx->d_tree_o) + b_to);
+    ctx->d_tree_pos = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctx->d_tree_ml) + b_tml);
     // theta_i = rope_base^(-2i/d) once, in fp64 on the host
     double theta[64];
     for (int i = 0; i < cfg->head_dim / 2; ++i) theta[i] = pow(cfg->rope_base, (-2.0 * i) / cfg->head_dim);
@@ -537,14 +572,7 @@ pkv_status pkv_decode_attn_varlen(pkv_ctx* ctx, const void* q, const void* k_poo
                                 stream) != cudaSuccess)
         return PKV_ERR_CUDA;
     if (citems > 0) {
-        if (ctx->tp_k_ptr != k_pool) {
-            if (!encode_pool_rows(ctx, k_pool, ctx->cfg.page_size, &ctx->tpk)) return PKV_ERR_CUDA;
-            ctx->tp_k_ptr = k_pool;
-        }
-        if (ctx->tp_v_ptr != v_pool) {
-            if (!encode_pool_rows(ctx, v_pool, ctx->cfg.page_size, &ctx->tpv)) return PKV_ERR_CUDA;
-            ctx->tp_v_ptr = v_pool;
-        }
+        if (!pkv::page_maps(ctx, k_pool, v_pool)) return PKV_ERR_CUDA;
         pkv::AttnParams cp;
         cp.q = static_cast<const __nv_bfloat16*>(q);
         cp.out = static_cast<__nv_bfloat16*>(out);

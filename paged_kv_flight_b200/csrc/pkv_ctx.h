@@ -37,10 +37,19 @@ struct pkv_ctx {
     const void* t16_k_ptr;
     const void* t16_v_ptr;
     CUtensorMap t16k, t16v;
-    // page-high boxes (P rows) for the prefill-chunk kernel (bf16 pools)
+    // page-high boxes (P rows) for the prefill-chunk kernel (bf16 pools) and
+    // the tree attention
     const void* tp_k_ptr;
     const void* tp_v_ptr;
     CUtensorMap tpk, tpv;
+    // pkv_decode_attn_tree: CTAs, the parts of items they share, the view of q
+    int tree_runs;
+    float* d_tree_o;
+    float2* d_tree_ml;
+    int4* d_tree_pos;
+    const void* tq_ptr;
+    int tq_tokens;
+    CUtensorMap tq;
     const void* tm_w_ptr;        // QKV weight and input maps of pkv_qkv_rope_append
     int tm_w_hidden, tm_w_layout;
     int qkv_split;               // 0: automatic
@@ -63,5 +72,12 @@ pkv_status check_call(const pkv_ctx* ctx, int batch, int bt_stride, const void* 
 // 2-D TMA view of a pool (rows = num_pages * Hkv * P token rows of head_dim
 // elements), boxes of box_rows rows x (128 or 64 bytes), swizzled.
 bool encode_pool_rows(const pkv_ctx* ctx, const void* pool, int box_rows, CUtensorMap* map);
+
+// The context's page-high maps of both pools, encoded when a pool is new.
+bool page_maps(pkv_ctx* ctx, const void* k_pool, const void* v_pool);
+
+// 3-D TMA view of q [n_tokens][Hq][head_dim] bf16, boxes of `tokens` tokens x
+// one group's heads x 64 elements, 128-byte swizzle.
+bool encode_q_rows(const pkv_ctx* ctx, const void* q, int n_tokens, int tokens, CUtensorMap* map);
 
 }  // namespace pkv

@@ -167,6 +167,14 @@ pkv_status pkv_decode_attn_tree(pkv_ctx* ctx, const void* q, const void* k_pool,
     const pkv_status dev = check_device(ctx);
     if (dev != PKV_OK) return dev;
 
+    const int tb = pkv::kTreeRows / ctx->G;
+    if (!pkv::page_maps(ctx, k_pool, v_pool)) return PKV_ERR_CUDA;
+    if (ctx->tq_ptr != q || ctx->tq_tokens != n_tokens) {
+        if (!pkv::encode_q_rows(ctx, q, n_tokens, tb, &ctx->tq)) return PKV_ERR_CUDA;
+        ctx->tq_ptr = q;
+        ctx->tq_tokens = n_tokens;
+    }
+
     pkv::TreeAttnParams p;
     p.q = static_cast<const __nv_bfloat16*>(q);
     p.out = static_cast<__nv_bfloat16*>(out);
@@ -189,7 +197,12 @@ pkv_status pkv_decode_attn_tree(pkv_ctx* ctx, const void* q, const void* k_pool,
     p.num_pages = ctx->cfg.num_pages;
     p.mask_words = mask_words;
     p.n_tokens = n_tokens;
-    return launched(pkv::launch_tree_attn(p, ctx->cfg.head_dim, ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3, stream));
+    p.part_o = ctx->d_tree_o;
+    p.part_ml = ctx->d_tree_ml;
+    p.pos = ctx->d_tree_pos;
+    p.tb = tb;
+    return launched(pkv::launch_tree_attn(p, ctx->tq, ctx->tpk, ctx->tpv, ctx->cfg.head_dim,
+                                          ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3, ctx->tree_runs, stream));
 }
 
 pkv_status pkv_tree_commit(pkv_ctx* ctx, void* k_pool, void* v_pool, const float* k_scale, const float* v_scale,

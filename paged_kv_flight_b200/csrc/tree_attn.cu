@@ -1,134 +1,957 @@
 // tree_attn.cu -- attention of a tree of drafted tokens over the paged cache
-// (pkv_decode_attn_tree).
+// on the tensor cores (pkv_decode_attn_tree): S, P and O in tensor memory
+// (tcgen05), Q and the K / V pages by TMA into shared memory.
 //
 // "Scaling TensorRT-LLM: Kernel Fusion and Inflight Batching in Production",
 // section "3. Speculative Decoding for Tail Latency" (a draft proposes tokens
-// and the target model checks all of them in one forward pass).
+// and the target model checks all of them in one forward pass); "TensorRT-LLM
+// Guide: High-Throughput GPU Inference Engine", section "3. Custom Fused
+// Attention Kernels: FMHA and XQA" (K / V read once for a group's heads).
 //
-// One CTA per (new token, kv head), the G query heads of the group together;
-// its warps take the keys in turn, each with a running maximum and sum per
-// head, and are merged at the end.
+// Mathematics: o = softmax(q K^T / sqrt(d)) V over the keys a row sees, all
+// cached keys and those drafted ones whose mask bit is set.  One pass with a
+// running reference m and sum l per row: S = Q K^T, P = 2^(s - m), l += P,
+// O += P V; a row's m moves only when its maximum passes it by more than 2^8,
+// then O and l are rescaled in place.
+//
+// Work item: a request, one of its kv heads and a block of up to 2 (128 / G)
+// of its new tokens; the G heads of the group times the tokens are the rows
+// of the MMAs, 128 in each of two streams.  A stream has its own S / P buffer
+// and O in tensor memory and its own four softmax warps, so one stream's
+// softmax runs while the other's MMAs do.  With more than 128 rows the streams
+// take one half of the rows each and share every K / V tile ("row mode": the
+// cache is read once per 256 rows); with at most 128 they take the even and
+// the odd key tiles of the same rows and are merged at the end ("key mode").
+//
+// The items' tiles of 128 keys, in order, are cut into as many runs as there
+// are SMs, of equal cost; a run's first and last item may be parts, whose
+// unnormalised O, m and l go to the workspace and are merged by tree_combine
+// in a fixed order.  Nothing waits for another CTA.
+//
+// Warps: 0 loads (TMA), 1 issues the MMAs, 2 .. 9 softmax and output, one
+// thread per row; for E4M3 pools 10 .. 13 turn the codes into bf16 tiles
+// (exact; the scales of a page and head go into the scores and the weights in
+// fp32).  P goes to the MMA as two bf16 terms P_hi + P_lo (about 16
+// significant bits), so that a row with few keys carries no error of bf16's
+// size beyond its own rounding.
 #include "tree_params.h"
 #include "pkv_device.cuh"
+#include "umma.cuh"
 
 namespace pkv {
 namespace {
 
 using namespace dev;
 
-constexpr int kTreeWarps = 4;
+constexpr int kTRows = 128;                   // rows of a stream
+constexpr int kTKeys = 128;                   // keys of a tile
+constexpr int kTBlk = kTRows * 128;           // 64 columns of a 128-row tile in bf16: 16 KB
+constexpr uint32_t kTCols = 512;              // tensor memory: S / P of two streams, O of two streams
+constexpr uint32_t kTOcol = 2 * kTKeys;
+constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
+// Relative cost of a tile for the cut: in row mode it has twice the softmax
+// and MMA work of key mode on the same bytes.
+constexpr int kCostRow = 3, kCostKey = 2;
+constexpr int kSnap = 2;                      // a cut this near to an item's ends moves there
 
 template <int D, bool FP8>
-__global__ void __launch_bounds__(kTreeWarps * 32) tree_attn_kernel(const TreeAttnParams p)
+struct TreeGeo {
+    static constexpr int KB = D / 64;
+    static constexpr int SLOT = KB * kTBlk;                          // K or V of a tile in bf16
+    static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+    static constexpr int NC = FP8 ? (D == 128 ? 4 : 6) : 0;          // tiles of codes
+    static constexpr int STG = kTKeys * D;
+    static constexpr int THREADS = 64 + 256 + (FP8 ? 128 : 0);
+    static constexpr int BYTES = (2 + NS) * SLOT + NC * STG + 1024;
+};
+
+// ---- the cut ------------------------------------------------------------------
+
+struct Request {
+    int row0, T, L, NT;
+};
+
+// 0: nothing to do; 1: ok; 2: cu_q out of range; 3: lengths out of range
+// (its rows are zero).
+__device__ __forceinline__ int read_request(const TreeAttnParams& p, int b, Request& r)
 {
-    constexpr int E = D / 32;            // elements of a row per lane
-    __shared__ float s_o[kTreeWarps][kMaxGroup][D], s_m[kTreeWarps][kMaxGroup], s_l[kTreeWarps][kMaxGroup];
-    const int row = blockIdx.x, kvh = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    int lo = 0, hi = p.batch;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (p.cu_q[mid] <= row) lo = mid;
-        else hi = mid;
+    const int a = p.cu_q[b], e = p.cu_q[b + 1];
+    if (a < 0 || e > p.n_tokens || a > e) return 2;
+    r.row0 = a;
+    r.T = e - a;
+    if (r.T == 0) return 0;
+    r.L = p.seq_lens[b];
+    const long long keys = (long long)r.L + r.T;
+    if (r.L < 0 || keys > (long long)p.bt_stride * p.P || r.T > 32ll * p.mask_words) return 3;
+    r.NT = (int)((keys + kTKeys - 1) / kTKeys);
+    return 1;
+}
+
+// Blocks of 2 tb tokens: those in row mode (more than tb tokens), then at
+// most one in key mode.
+__device__ __forceinline__ void blocks_of(const TreeAttnParams& p, int T, int& row_blocks, int& blocks)
+{
+    const int two = 2 * p.tb;
+    row_blocks = T / two + (T % two > p.tb ? 1 : 0);
+    blocks = (T + two - 1) / two;
+}
+
+__device__ __forceinline__ long long cost_of(const TreeAttnParams& p, const Request& r)
+{
+    int rb, nb;
+    blocks_of(p, r.T, rb, nb);
+    return (long long)p.Hkv * r.NT * ((long long)rb * kCostRow + (nb - rb) * kCostKey);
+}
+
+// A place in the order of all tiles: request, kv head, block, tile.
+__device__ __forceinline__ bool before(const int4& a, const int4& b)
+{
+    return a.x != b.x ? a.x < b.x : a.y != b.y ? a.y < b.y : a.z != b.z ? a.z < b.z : a.w < b.w;
+}
+__device__ __forceinline__ bool same_item(const int4& a, const int4& b) { return a.x == b.x && a.y == b.y && a.z == b.z; }
+
+__device__ __forceinline__ int4 next_item(int b, int kvh, int blk, int blocks, int Hkv)
+{
+    if (++blk < blocks) return make_int4(b, kvh, blk, 0);
+    if (++kvh < Hkv) return make_int4(b, kvh, 0, 0);
+    return make_int4(b + 1, 0, 0, 0);
+}
+
+// The place at cost `at` of request b, moved to an item's start or end when
+// it is near.
+__device__ __forceinline__ int4 place_at(const TreeAttnParams& p, int b, const Request& r, long long at)
+{
+    int rb, nb;
+    blocks_of(p, r.T, rb, nb);
+    const long long row_cost = (long long)r.NT * kCostRow, head = row_cost * rb + (long long)(nb - rb) * r.NT * kCostKey;
+    const int kvh = (int)(at / head);
+    at -= head * kvh;
+    const int blk = (int)min(at / row_cost, (long long)rb);
+    at -= row_cost * blk;
+    const int tile = (int)(at / (blk < rb ? kCostRow : kCostKey));
+    if (tile <= kSnap) return make_int4(b, kvh, blk, 0);
+    if (r.NT - tile <= kSnap) return next_item(b, kvh, blk, nb, p.Hkv);
+    return make_int4(b, kvh, blk, tile);
+}
+
+// A run's share of one item: tiles t0 .. t0 + n - 1 of its NT.
+struct Segment {
+    int b, kvh, row0, ntok, L, T, NT, t0, n, units;
+    int place;             // 0: the whole item, 1: its start, 2: a later part
+    bool row_mode;
+};
+
+struct Walk {
+    int4 cur, end;
+    int at = -1;           // the request in r
+    Request r;
+    __device__ __forceinline__ bool next(const TreeAttnParams& p, Segment& s)
+    {
+        while (before(cur, end)) {
+            if (at != cur.x) {
+                at = cur.x;
+                if (read_request(p, at, r) != 1) {
+                    cur = make_int4(at + 1, 0, 0, 0);
+                    continue;
+                }
+            }
+            int rb, nb;
+            blocks_of(p, r.T, rb, nb);
+            const int first = cur.z * 2 * p.tb;
+            s.b = cur.x;
+            s.kvh = cur.y;
+            s.row0 = r.row0 + first;
+            s.ntok = min(2 * p.tb, r.T - first);
+            s.L = r.L;
+            s.T = r.T;
+            s.NT = r.NT;
+            s.row_mode = s.ntok > p.tb;
+            s.t0 = cur.w;
+            s.n = (same_item(cur, end) ? end.w : r.NT) - s.t0;
+            s.units = s.row_mode ? 2 * s.n : s.n;
+            s.place = s.n == r.NT ? 0 : s.t0 == 0 ? 1 : 2;
+            cur = next_item(cur.x, cur.y, cur.z, nb, p.Hkv);
+            return true;
+        }
+        return false;
     }
-    const int b = lo, a = p.cu_q[b], e = p.cu_q[b + 1];
-    if (a < 0 || e > p.n_tokens || a > e) {
-        if (tid == 0) atomicOr(p.err, kErrLength);
-        return;
-    }
-    if (row < a || row >= e) return;
-    const int L = p.seq_lens[b], T = e - a;
-    const bool ok = L >= 0 && (long long)L + T <= (long long)p.bt_stride * p.P && T <= 32 * p.mask_words;
-    if (!ok && tid == 0) atomicOr(p.err, kErrLength);
-    const int keys = ok ? L + T : 0;
-    float q[kMaxGroup][E], o[kMaxGroup][E], m[kMaxGroup], l[kMaxGroup];
+};
+
+// Place of a segment's loads in its sequence.  Unit u is tile u of stream u %
+// 2 in key mode, tile u / 2 of stream u % 2 in row mode; the MMAs go S(0),
+// S(1), then P V(u), S(u + 2) for every u, and the loads in the order of
+// their first use.
+__device__ __forceinline__ int k_seq(const Segment& s, int i) { return s.row_mode ? 2 * i : i < 2 ? i : 2 * i - 1; }
+__device__ __forceinline__ int v_seq(const Segment& s, int i) { return s.row_mode ? 2 * i + 1 : i + min(i + 2, s.n); }
+
+__device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
+// ---- softmax of one tile --------------------------------------------------------
+
+__device__ __forceinline__ bool bit(const uint32_t (&vis)[4], int c) { return (vis[c >> 5] >> (c & 31)) & 1u; }
+
+// Largest scaled score of the row in this tile.  kk: score scale in log2
+// units (E4M3: times the K scale, for every 16 keys).
+template <bool FP8, bool MASKED>
+__device__ __forceinline__ float tile_max(uint32_t scol, const uint32_t (&vis)[4], const float (&kk)[8])
+{
+    float mx = -INFINITY;
 #pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g) {
-        m[g] = -INFINITY;
-        l[g] = 0.f;
+    for (int c0 = 0; c0 < kTKeys; c0 += 64) {
+        uint32_t sa[32], sb[32];
+        tmem_ld32(scol + (uint32_t)c0, sa);
+        tmem_ld32(scol + (uint32_t)c0 + 32u, sb);
+        tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            o[g][i] = 0.f;
-            q[g][i] = g < p.G ? __bfloat162float(p.q[((size_t)row * p.Hq + kvh * p.G + g) * D + lane + 32 * i]) : 0.f;
+        for (int k = 0; k < 4; ++k) {              // 16 keys at a time
+            float g = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 16; ++c) {
+                const float x = __uint_as_float(k < 2 ? sa[16 * k + c] : sb[16 * (k - 2) + c]);
+                g = fmaxf(g, !MASKED || bit(vis, c0 + 16 * k + c) ? x : -INFINITY);
+            }
+            mx = fmaxf(mx, FP8 ? g * kk[c0 / 16 + k] : g);
         }
     }
-    for (int j = warp; j < keys; j += kTreeWarps) {
-        const int d = j - L;
-        if (d >= 0 && !((p.tree_mask[(size_t)row * p.mask_words + d / 32] >> (d & 31)) & 1u)) continue;
-        const int page = p.block_tables[(size_t)b * p.bt_stride + j / p.P];
-        if ((unsigned)page >= (unsigned)p.num_pages) {
-            if (lane == 0) atomicOr(p.err, kErrPage);
-            continue;
-        }
-        const size_t at = (((size_t)page * p.Hkv + kvh) * p.P + j % p.P) * D;
-        float k[E], v[E], ks = 1.f, vs = 1.f;
-        if (FP8) {
-            ks = p.k_scale[(size_t)page * p.Hkv + kvh];
-            vs = p.v_scale[(size_t)page * p.Hkv + kvh];
-        }
+    return FP8 ? mx : mx * kk[0];
+}
+
+// P = 2^(s - m) over the row's S columns as P_hi + P_lo, 32 keys at a time:
+// keys c0 + 2i, + 1 in column c0 + i (P_hi) and c0 + 16 + i (P_lo).  E4M3: P
+// times the V scale.  Returns the sum of the weights.
+template <bool FP8, bool MASKED>
+__device__ __forceinline__ float tile_weights(uint32_t scol, const uint32_t (&vis)[4], const float (&kk)[8],
+                                              const float (&vs)[8], float m)
+{
+    float sum0 = 0.f, sum1 = 0.f;
+    uint32_t sv[2][32];
+    tmem_ld32(scol, sv[0]);
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            if (FP8) {
-                const __nv_fp8_storage_t kc = reinterpret_cast<const uint8_t*>(p.k_pool)[at + lane + 32 * i];
-                const __nv_fp8_storage_t vc = reinterpret_cast<const uint8_t*>(p.v_pool)[at + lane + 32 * i];
-                k[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(kc, __NV_E4M3))) * ks;
-                v[i] = __half2float(__half(__nv_cvt_fp8_to_halfraw(vc, __NV_E4M3))) * vs;
-            } else {
-                k[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.k_pool)[at + lane + 32 * i]);
-                v[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v_pool)[at + lane + 32 * i]);
+    for (int k32 = 0; k32 < 4; ++k32) {
+        const int c0 = 32 * k32;
+        tmem_wait_ld();
+        if (k32 < 3) tmem_ld32(scol + (uint32_t)c0 + 32u, sv[(k32 + 1) & 1]);
+        uint32_t(&s)[32] = sv[k32 & 1];
+#pragma unroll
+        for (int k16 = 0; k16 < 2; ++k16) {
+            const float f = FP8 ? kk[2 * k32 + k16] : kk[0];
+            uint32_t hi[8], lo[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = 16 * k16 + 2 * i;
+                float p0 = ex2(fmaf(__uint_as_float(s[c]), f, -m));
+                float p1 = ex2(fmaf(__uint_as_float(s[c + 1]), f, -m));
+                if (MASKED) {
+                    p0 = bit(vis, c0 + c) ? p0 : 0.f;
+                    p1 = bit(vis, c0 + c + 1) ? p1 : 0.f;
+                }
+                sum0 += p0;
+                sum1 += p1;
+                if (FP8) {
+                    p0 *= vs[2 * k32 + k16];
+                    p1 *= vs[2 * k32 + k16];
+                    if (MASKED) {          // 0 x a scale that is no number
+                        p0 = bit(vis, c0 + c) ? p0 : 0.f;
+                        p1 = bit(vis, c0 + c + 1) ? p1 : 0.f;
+                    }
+                }
+                hi[i] = pack_bf16(p0, p1);
+                lo[i] = pack_bf16(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
+            }
+            tmem_st8(scol + (uint32_t)(c0 + 8 * k16), hi);
+            tmem_st8(scol + (uint32_t)(c0 + 16 + 8 * k16), lo);
+        }
+    }
+    return sum0 + sum1;
+}
+
+// ---- the kernel -------------------------------------------------------------------
+
+template <int D, bool FP8>
+__global__ void __launch_bounds__(TreeGeo<D, FP8>::THREADS, 1)
+tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                 const __grid_constant__ CUtensorMap tmv, const TreeAttnParams p)
+{
+    using Gm = TreeGeo<D, FP8>;
+    constexpr int KB = Gm::KB, NS = Gm::NS, NCX = FP8 ? Gm::NC : 1, SLOT = Gm::SLOT;
+    constexpr int THREADS = Gm::THREADS, WARPS = THREADS / 32;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t s_full[NS], s_empty[NS], s_cfull[NCX], s_cempty[NCX];
+    __shared__ __align__(8) uint64_t s_qfull[2], s_qempty[2], s_sfull[2], s_pfull[2], s_ofin[2], s_drain;
+    __shared__ float2 s_ml[kTRows];
+    __shared__ long long s_scan[WARPS];
+    __shared__ int4 s_pos[2];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_bad, s_fail, s_odd;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int cta = blockIdx.x, W = gridDim.x;
+    grid_launch_dependents();
+
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t q0 = base, ring = base + 2u * SLOT, stage = ring + (uint32_t)(NS * SLOT);
+    const uint32_t full = smem_u32(s_full), empty = smem_u32(s_empty), cfull = smem_u32(s_cfull),
+                   cempty = smem_u32(s_cempty), qfull = smem_u32(s_qfull), qempty = smem_u32(s_qempty),
+                   sfull = smem_u32(s_sfull), pfull = smem_u32(s_pfull), ofin = smem_u32(s_ofin),
+                   drain = smem_u32(&s_drain);
+
+    // ---- where this CTA's run starts and ends
+    {
+        const int per = (p.batch + THREADS - 1) / THREADS;
+        const int lo = min(p.batch, tid * per), hi = min(p.batch, lo + per);
+        long long mine = 0;
+        int err = 0;
+        Request r;
+        for (int b = lo; b < hi; ++b) {
+            const int st = read_request(p, b, r);
+            if (st == 1) mine += cost_of(p, r);
+            else if (st) err = kErrLength;
+        }
+        if (err && cta == 0) atomicOr(p.err, err);
+        long long incl = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += y;
+        }
+        if (lane == 31) s_scan[warp] = incl;
+        if (tid < 2) s_pos[tid] = make_int4(p.batch, 0, 0, 0);
+        __syncthreads();
+        long long pre = incl - mine, total = 0;
+        for (int w = 0; w < WARPS; ++w) {
+            if (w < warp) pre += s_scan[w];
+            total += s_scan[w];
+        }
+        for (int k = 0; k < 2; ++k) {
+            const long long x = total * (cta + k) / W;
+            if (x < pre || x >= pre + mine) continue;
+            long long at = pre;
+            for (int b = lo; b < hi; ++b) {
+                if (read_request(p, b, r) != 1) continue;
+                const long long c = cost_of(p, r);
+                if (x < at + c) {
+                    s_pos[k] = place_at(p, b, r, x - at);
+                    break;
+                }
+                at += c;
             }
         }
-#pragma unroll
-        for (int g = 0; g < kMaxGroup; ++g) {
-            if (g >= p.G) break;
-            float s = 0.f;
-#pragma unroll
-            for (int i = 0; i < E; ++i) s += q[g][i] * k[i];
-#pragma unroll
-            for (int w = 16; w > 0; w >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, w);
-            s *= p.scale_log2;
-            const float mn = fmaxf(m[g], s), al = exp2f(m[g] - mn), pr = exp2f(s - mn);
-            m[g] = mn;
-            l[g] = l[g] * al + pr;
-#pragma unroll
-            for (int i = 0; i < E; ++i) o[g][i] = o[g][i] * al + pr * v[i];
+        __syncthreads();
+        if (tid < 2 && (tid == 0 || cta == W - 1)) p.pos[cta + tid] = s_pos[tid];
+        // rows of requests whose lengths are out of range
+        for (int b = cta; b < p.batch; b += W) {
+            if (read_request(p, b, r) != 3) continue;
+            uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)r.row0 * p.Hq * D);
+            const size_t n = (size_t)r.T * p.Hq * D / 8;
+            for (size_t i = tid; i < n; i += THREADS) dst[i] = make_uint4(0u, 0u, 0u, 0u);
         }
     }
-#pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g) {
-#pragma unroll
-        for (int i = 0; i < E; ++i) s_o[warp][g][lane + 32 * i] = o[g][i];
-        if (lane == 0) {
-            s_m[warp][g] = m[g];
-            s_l[warp][g] = l[g];
+    Walk walk;
+    walk.cur = s_pos[0];
+    walk.end = s_pos[1];
+    if (!before(walk.cur, walk.end)) return;      // the whole CTA
+
+    if (tid == 0) {
+        s_bad = 0;
+        s_fail = 0;
+        s_odd = 0;
+        prefetch_tensormap(&tmq);
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + 8u * i, FP8 ? 4u : 1u);
+            mbar_init(empty + 8u * i, 1u);
         }
+        for (int i = 0; FP8 && i < NCX; ++i) {
+            mbar_init(cfull + 8u * i, 1u);
+            mbar_init(cempty + 8u * i, 4u);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull + 8u * i, 1u);
+            mbar_init(qempty + 8u * i, 1u);
+            mbar_init(sfull + 8u * i, 1u);
+            mbar_init(pfull + 8u * i, 4u);
+            mbar_init(ofin + 8u * i, 1u);
+        }
+        mbar_init(drain, 1u);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(smem_u32(&s_tmem), kTCols);
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = s_tmem;
+    Segment s;
+
+    if (warp == 0) {
+        // ---- loads
+        constexpr int N = FP8 ? NCX : NS;
+        constexpr int ROWB = FP8 ? D : 2 * D;                // bytes of a row in the pool
+        const uint32_t lfull = FP8 ? cfull : full, lempty = FP8 ? cempty : empty, dst0 = FP8 ? stage : ring;
+        constexpr int LSLOT = FP8 ? Gm::STG : SLOT;
+        constexpr int LB = FP8 ? 1 : KB, LBLK = kTBlk;       // TMA boxes across a row
+        const int ppt = kTKeys / p.P;
+        int ld = 0, qc0 = 0, qc1 = 0, qsel = 0;
+        bool ok = true;
+        while (ok && walk.next(p, s)) {
+            const int n_keys = s.L + s.T;
+            const int32_t* bt = p.block_tables + (size_t)s.b * p.bt_stride;
+            auto page_of = [&](int i) {                      // this lane's page of tile i; -1: out of range, -2: none
+                const int at = (s.t0 + i) * ppt + lane;
+                if (i >= s.n || lane >= ppt || at * p.P >= n_keys) return -2;
+                const int page = __ldg(&bt[at]);
+                return (unsigned)page < (unsigned)p.num_pages ? page : -1;
+            };
+            int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2);
+            auto load = [&](const CUtensorMap* map, int page) {
+                const int j = ld % N;
+                if (ld >= N) ok = __all_sync(0xffffffffu, mbar_wait_bounded(lempty + 8u * j, (uint32_t)((ld / N - 1) & 1), kTWaitNs));
+                if (!ok) return;
+                const bool have = page != -2;
+                if (page == -1) {
+                    s_bad = 1;                               // its keys are masked; an in-range page keeps the copy legal
+                    atomicOr(p.err, kErrPage);
+                    page = 0;
+                }
+                const int np = __popc(__ballot_sync(0xffffffffu, have));
+                if (lane == 0) mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
+                __syncwarp();
+                if (have) {
+                    const uint32_t dst = dst0 + (uint32_t)(j * LSLOT + lane * p.P * (FP8 ? D : 128));
+                    const int y = (page * p.Hkv + s.kvh) * p.P;
+#pragma unroll
+                    for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * LBLK), map, 64 * kb, y, lfull + 8u * j);
+                }
+                ++ld;
+            };
+            auto load_q = [&](int buf, int& count, int token) {
+                if (count > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(qempty + 8u * buf, (uint32_t)((count - 1) & 1), kTWaitNs));
+                if (!ok) return;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(qfull + 8u * buf, (uint32_t)(KB * 128 * p.tb * p.G));
+#pragma unroll
+                    for (int kb = 0; kb < KB; ++kb)
+                        tma_load_3d(q0 + (uint32_t)(buf * SLOT + kb * kTBlk), &tmq, 64 * kb, s.kvh * p.G, token, qfull + 8u * buf);
+                }
+                __syncwarp();
+                ++count;
+            };
+            int ik = 0, iv = 0;
+            const int lead = s.row_mode ? 1 : 2;
+            while (ok && iv < s.n) {
+                if (ik < s.n && ik < iv + lead) {
+                    load(&tmk, ik == iv ? pg0 : pg1);
+                    ++ik;
+                } else {
+                    load(&tmv, pg0);
+                    ++iv;
+                    pg0 = pg1;
+                    pg1 = pg2;
+                    pg2 = page_of(iv + 2);
+                }
+                if (ok && ik + iv == 2) {      // the first tiles are under way: now Q, once it is free
+                    if (s.row_mode) {
+                        load_q(0, qc0, s.row0);
+                        load_q(1, qc1, s.row0 + p.tb);
+                    } else {
+                        if (qsel == 0) load_q(0, qc0, s.row0);
+                        else load_q(1, qc1, s.row0);
+                        qsel ^= 1;
+                    }
+                }
+            }
+        }
+        if (!ok || *(volatile int*)&s_fail) {
+            // copies under way land before the CTA's memory is given back
+            s_fail = 1;
+            for (int j = max(0, ld - N); j < ld; ++j)
+                (void)mbar_wait_bounded(lfull + 8u * (j % N), (uint32_t)((j / N) & 1), kTWaitNs);
+            if (qc0 > 0) (void)mbar_wait_bounded(qfull, (uint32_t)((qc0 - 1) & 1), kTWaitNs);
+            if (qc1 > 0) (void)mbar_wait_bounded(qfull + 8u, (uint32_t)((qc1 - 1) & 1), kTWaitNs);
+        }
+    } else if (warp == 1) {
+        // ---- MMA issue, one thread
+        if (lane == 0) {
+            constexpr uint32_t idS = umma_idesc_bf16<kTRows, kTKeys>();
+            constexpr uint32_t idO = umma_idesc_bf16<kTRows, D, true>();
+            int rb = 0, qsel = 0;
+            int qc[2] = {0, 0}, pc[2] = {0, 0};
+            bool ok = true;
+            auto wait = [&](uint32_t bar, int phase) {
+                ok = ok && mbar_wait_bounded(bar, (uint32_t)(phase & 1), kTWaitNs);
+            };
+            while (ok && walk.next(p, s)) {
+                auto score = [&](int u) {
+                    const int st = u & 1, i = s.row_mode ? u >> 1 : u;
+                    const int seq = rb + k_seq(s, i), slot = seq % NS;
+                    const int qb = s.row_mode ? st : qsel;
+                    if (u == 0 || (u == 1 && s.row_mode)) wait(qfull + 8u * qb, qc[qb]++);
+                    wait(full + 8u * slot, seq / NS);
+                    if (!ok) return;
+                    tmem_fence_after();
+                    const uint32_t qa = q0 + (uint32_t)(qb * SLOT), ka = ring + (uint32_t)(slot * SLOT);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint32_t off = (uint32_t)((kk >> 2) * kTBlk + (kk & 3) * 32);
+                        umma_bf16(tmem + (uint32_t)(st * kTKeys), sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off),
+                                  idS, kk ? 1u : 0u);
+                    }
+                    umma_commit(sfull + 8u * st);
+                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
+                    if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) umma_commit(qempty + 8u * qb);
+                };
+                auto values = [&](int u) {
+                    const int st = u & 1, i = s.row_mode ? u >> 1 : u;
+                    const int seq = rb + v_seq(s, i), slot = seq % NS;
+                    wait(pfull + 8u * st, pc[st]++);
+                    wait(full + 8u * slot, seq / NS);
+                    if (!ok) return;
+                    tmem_fence_after();
+                    const uint32_t va = ring + (uint32_t)(slot * SLOT);
+                    const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
+#pragma unroll
+                    for (int kk = 0; kk < 2 * kTKeys / 16; ++kk) {      // 16 keys each: P_hi, then P_lo
+                        const int k8 = kk & 7;
+                        umma_bf16_ts(ocol, pcol + (uint32_t)((k8 >> 1) * 32 + (k8 & 1) * 8 + (kk >> 3) * 16),
+                                     sw128_mnmajor_desc(va + (uint32_t)(k8 * 2048), (uint32_t)kTBlk, 1024u), idO,
+                                     (kk || u >= 2) ? 1u : 0u);
+                    }
+                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
+                    if (u >= s.units - 2) umma_commit(ofin + 8u * st);
+                };
+                score(0);
+                if (s.units > 1) score(1);
+                for (int u = 0; ok && u < s.units; ++u) {
+                    values(u);
+                    if (u + 2 < s.units) score(u + 2);
+                }
+                if (!s.row_mode) qsel ^= 1;
+                rb += 2 * s.n;
+            }
+            if (!ok) s_fail = 1;
+            umma_commit(drain);              // every MMA has ended before the tensor memory is given back
+            (void)mbar_wait_bounded(drain, 0u, kTWaitNs);
+        }
+        __syncwarp();
+    } else if (warp < 10) {
+        // ---- softmax and output: row r of stream st
+        const int st = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+        const int rtok = r / p.G, g = r - rtok * p.G;
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        const uint32_t scol = lanes + (uint32_t)(st * kTKeys);
+        const int shift = 31 - __clz(p.P);
+        int rb = 0, sc = 0, oc0 = 0, oc1 = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, int phase) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)(phase & 1), kTWaitNs)) != 0;
+        };
+        auto pair = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };   // the two warps of these lanes
+        while (walk.next(p, s)) {
+            const int tok0 = s.row_mode ? st * p.tb : 0;
+            const int rows = min(p.tb, s.ntok - tok0) * p.G;
+            const bool valid = r < rows, act = 32 * quarter < rows;
+            const int n_keys = s.L + s.T;
+            const int32_t* bt = p.block_tables + (size_t)s.b * p.bt_stride;
+            const size_t trow = (size_t)s.row0 + tok0 + rtok;
+            const uint32_t* mrow = p.tree_mask + (valid ? trow : (size_t)s.row0) * p.mask_words;
+            // word i of the drafted keys this row sees; all cached keys before them
+            auto seen = [&](int i) -> uint32_t {
+                if (i < 0) return ~0u;
+                if (!valid || 32 * i >= s.T) return 0u;
+                return __ldg(&mrow[i]) & (s.T - 32 * i < 32 ? (1u << (s.T - 32 * i)) - 1u : ~0u);
+            };
+            // E4M3: lanes 0 .. 7 hold the K scales of a tile's pages, 8 .. 15 the V scales, one tile ahead
+            const int step = s.row_mode ? 1 : 2, first = s.row_mode ? 0 : st;
+            auto page_of = [&](int i) {
+                const int at = ((s.t0 + i) << (7 - shift)) + (lane & 7);
+                return FP8 && i < s.n && lane < 16 && at * p.P < n_keys && (lane & 7) < (kTKeys >> shift) ? __ldg(&bt[at]) : -1;
+            };
+            auto scale_of = [&](int page) {
+                return FP8 && (unsigned)page < (unsigned)p.num_pages
+                           ? __ldg(&(lane < 8 ? p.k_scale : p.v_scale)[(size_t)page * p.Hkv + s.kvh])
+                           : 0.f;
+            };
+            float scale_next = 0.f;
+            int page_next = -1;
+            if (FP8) {
+                scale_next = scale_of(page_of(first));
+                page_next = page_of(first + step);
+            }
+            float m = -INFINITY, l = 0.f;
+            for (int u = st; u < s.units; u += 2) {
+                const int i = s.row_mode ? u >> 1 : u, key0 = (s.t0 + i) * kTKeys;
+                float kk[8], vs[8];
+                if (FP8) {
+                    const float cur = scale_next;
+                    scale_next = scale_of(page_next);
+                    page_next = page_of(i + 2 * step);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        kk[k] = __shfl_sync(0xffffffffu, cur, (16 * k) >> shift) * p.scale_log2;
+                        vs[k] = __shfl_sync(0xffffffffu, cur, 8 + ((16 * k) >> shift));
+                    }
+                } else {
+                    kk[0] = p.scale_log2;
+                }
+                wait(sfull + 8u * st, sc++);
+                tmem_fence_after();
+                const bool bad = *(volatile int*)&s_bad != 0;
+                const bool tail = key0 + kTKeys > s.L;
+                if (ok && act) {
+                    uint32_t vis[4];
+                    if (tail || bad) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const int d0 = key0 - s.L + 32 * w;
+                            vis[w] = __funnelshift_r(seen(d0 >> 5), seen((d0 >> 5) + 1), d0 & 31);
+                        }
+                        for (int k = 0; bad && k < (kTKeys >> shift); ++k) {
+                            const int at = (key0 >> shift) + k;
+                            if (at * p.P >= n_keys || (unsigned)__ldg(&bt[at]) < (unsigned)p.num_pages) continue;
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                for (int c = 0; c < 32; ++c)
+                                    if (((32 * w + c) >> shift) == k) vis[w] &= ~(1u << c);
+                        }
+                    }
+                    const float mx = tail || bad ? tile_max<FP8, true>(scol, vis, kk) : tile_max<FP8, false>(scol, vis, kk);
+                    if (u < 2) {
+                        m = mx;
+                    } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+                        // S of this tile was issued after the last P V of the stream: O is settled
+                        const float mn = fmaxf(m, mx), alpha = m == mn ? 1.f : ex2(m - mn);
+#pragma unroll
+                        for (int c0 = 0; c0 < D; c0 += 32) {
+                            uint32_t o[32];
+                            const uint32_t oc = lanes + kTOcol + (uint32_t)(st * 128 + c0);
+                            tmem_ld32(oc, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+#pragma unroll
+                            for (int c = 0; c < 32; c += 8) tmem_st8(oc + (uint32_t)c, *reinterpret_cast<const uint32_t(*)[8]>(&o[c]));
+                        }
+                        l *= alpha;
+                        m = mn;
+                    }
+                    const float mref = m == -INFINITY ? 0.f : m;
+                    l += tail || bad ? tile_weights<FP8, true>(scol, vis, kk, vs, mref)
+                                     : tile_weights<FP8, false>(scol, vis, kk, vs, mref);
+                    tmem_wait_st();
+                }
+                if (tail && (!s.row_mode || st == 0)) {
+                    // V rows behind the last key hold anything: zero them, so that
+                    // 0 x V stays 0; and the numbers of drafted tokens that are not
+                    // finite, which rows that see them take back at the end
+                    const int seq = rb + v_seq(s, i), slot = seq % NS;
+                    wait(full + 8u * slot, seq / NS);
+                    const uint32_t va = ring + (uint32_t)(slot * SLOT);
+                    const int z0 = n_keys - key0, d0 = max(0, s.L - key0);
+                    if (ok) {
+                        bool wrote = false;
+                        for (int x = 32 * quarter + lane; x < (kTKeys - d0) * KB * 8; x += 128) {
+                            const int row = d0 + x / (KB * 8), rem = x % (KB * 8);
+                            const uint32_t addr = va + (uint32_t)((rem >> 3) * kTBlk + row * 128 + (rem & 7) * 16);
+                            if (row >= z0) {
+                                sts128(addr, make_uint4(0u, 0u, 0u, 0u));
+                                wrote = true;
+                                continue;
+                            }
+                            const uint4 v = lds128(addr);
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                            bool odd = false;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                if ((w[k] & 0x7F80u) == 0x7F80u) {
+                                    w[k] &= 0xFFFF0000u;
+                                    odd = true;
+                                }
+                                if ((w[k] & 0x7F800000u) == 0x7F800000u) {
+                                    w[k] &= 0xFFFFu;
+                                    odd = true;
+                                }
+                            }
+                            if (odd) {
+                                sts128(addr, make_uint4(w[0], w[1], w[2], w[3]));
+                                s_odd = 1;
+                                wrote = true;
+                            }
+                        }
+                        if (wrote) fence_proxy_async_smem();
+                    }
+                }
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pfull + 8u * st);
+            }
+
+            // ---- the end of the segment
+            if (s.row_mode) {
+                wait(ofin + 8u * st, st ? oc1 : oc0);
+                ++oc0;
+                ++oc1;
+            } else {
+                wait(ofin, oc0++);
+                if (s.n > 1) wait(ofin + 8u, oc1++);
+            }
+            tmem_fence_after();
+            float a0 = st == 0 ? 1.f : 0.f, a1 = 1.f - a0;
+            if (!s.row_mode) {
+                float2 other;
+                if (st == 1) s_ml[r] = make_float2(m, l);
+                pair();
+                if (st == 0) other = s_ml[r];
+                pair();
+                if (st == 0) s_ml[r] = make_float2(m, l);
+                pair();
+                if (st == 1) other = s_ml[r];
+                const float m0 = st == 0 ? m : other.x, m1 = st == 0 ? other.x : m;
+                const float l0 = st == 0 ? l : other.y, l1 = st == 0 ? other.y : l;
+                m = fmaxf(m0, m1);
+                a0 = m0 == -INFINITY ? 0.f : ex2(m0 - m);
+                a1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                l = l0 * a0 + l1 * a1;
+            }
+            if (ok && act) {
+                const bool both = !s.row_mode && s.n > 1;
+                const int cols = s.row_mode ? D : D / 2, col0 = s.row_mode ? 0 : st * (D / 2);
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const bool odd = *(volatile int*)&s_odd != 0;
+                const size_t slot_row = ((size_t)(2 * cta + (s.place == 1)) * 2 * kTRows) + (s.row_mode ? st * kTRows : 0) + r;
+                __nv_bfloat16* const orow = p.out + (trow * p.Hq + (size_t)s.kvh * p.G + g) * D;
+                if (valid && s.place && (s.row_mode || st == 0)) p.part_ml[slot_row] = make_float2(m, l);
+                for (int c0 = col0; c0 < col0 + cols; c0 += 32) {
+                    uint32_t x0[32];
+                    float o[32];
+                    tmem_ld32(lanes + kTOcol + (uint32_t)((s.row_mode ? st * 128 : 0) + c0), x0);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) o[c] = s.row_mode ? __uint_as_float(x0[c]) : a0 * __uint_as_float(x0[c]);
+                    if (both) {
+                        tmem_ld32(lanes + kTOcol + 128u + (uint32_t)c0, x0);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = fmaf(a1, __uint_as_float(x0[c]), o[c]);
+                    }
+                    if (odd && valid) {      // numbers that are not finite in V of the drafted tokens this row sees
+                        const int j1 = min(s.T, (s.t0 + s.n) * kTKeys - s.L);
+                        for (int j = max(0, s.t0 * kTKeys - s.L); j < j1; ++j) {
+                            if (!((seen(j >> 5) >> (j & 31)) & 1u)) continue;
+                            const int page = bt[(s.L + j) >> shift];
+                            if ((unsigned)page >= (unsigned)p.num_pages) continue;
+                            const size_t at = (((size_t)page * p.Hkv + s.kvh) * p.P + ((s.L + j) & (p.P - 1))) * D + c0;
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                float v;
+                                if (FP8) {
+                                    const __nv_fp8_storage_t code = reinterpret_cast<const uint8_t*>(p.v_pool)[at + c];
+                                    v = __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
+                                } else {
+                                    v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v_pool)[at + c]);
+                                }
+                                if (!isfinite(v)) o[c] += v;
+                            }
+                        }
+                    }
+                    if (!valid) continue;
+                    if (s.place == 0) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 8)
+                            *reinterpret_cast<uint4*>(orow + c0 + c) =
+                                make_uint4(pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
+                                           pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv));
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4)
+                            *reinterpret_cast<float4*>(p.part_o + slot_row * D + c0 + c) =
+                                make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                }
+            }
+            tmem_fence_before();
+            if (!s.row_mode) pair();         // both warps have read both streams' O
+            rb += 2 * s.n;
+        }
+        if (!ok) s_fail = 1;
+    } else if (FP8) {
+        // ---- codes to bf16: lane l of a warp takes row 8 k + l % 8, 16 codes l / 8 + 4 j
+        const int w = warp - 10;
+        int q = 0;
+        bool ok = true;
+        while (ok && walk.next(p, s)) {
+            for (int e = q + 2 * s.n; ok && q < e; ++q) {
+                const int c = q % NCX, slot = q % NS;
+                ok = __all_sync(0xffffffffu, mbar_wait_bounded(cfull + 8u * c, (uint32_t)((q / NCX) & 1), kTWaitNs)) != 0;
+                if (ok && q >= NS)
+                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + 8u * slot, (uint32_t)((q / NS - 1) & 1), kTWaitNs)) != 0;
+                if (!ok) break;
+                const uint32_t src = stage + (uint32_t)(c * Gm::STG), dst = ring + (uint32_t)(slot * SLOT);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int row = 32 * w + 8 * k + (lane & 7);
+#pragma unroll
+                    for (int j = 0; j < D / 64; ++j) {
+                        const int ch = (lane >> 3) + 4 * j;                  // 16 codes: d 16 ch ..
+                        const uint32_t at = D == 128 ? (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4))
+                                                     : (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
+                        const uint4 v = lds128(src + at);
+                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int x = 0; x < 4; ++x) {
+                            const float2 a = f16x2_to_f32(cvt_lo(in[x])), b = f16x2_to_f32(cvt_hi(in[x]));
+                            o[2 * x] = pack_bf16(a.x, a.y);
+                            o[2 * x + 1] = pack_bf16(b.x, b.y);
+                        }
+                        const uint32_t row_at = dst + (uint32_t)((ch >> 2) * kTBlk + row * 128);
+                        const int c16 = 2 * (ch & 3);
+                        sts128(row_at + (uint32_t)((c16 ^ (row & 7)) << 4), make_uint4(o[0], o[1], o[2], o[3]));
+                        sts128(row_at + (uint32_t)(((c16 + 1) ^ (row & 7)) << 4), make_uint4(o[4], o[5], o[6], o[7]));
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(full + 8u * slot);
+                    mbar_arrive(cempty + 8u * c);
+                }
+            }
+        }
+        if (!ok) s_fail = 1;
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_dealloc(tmem, kTCols);
+        if (lane == 0 && s_fail) atomicOr(p.err, kErrTimeout);
+    }
+}
+
+// ---- merge of the items that the cut went through -----------------------------------
+
+constexpr int kCombineThreads = 256;
+constexpr int kCombineGroups = 16;      // blocks per cut, each a share of the item's rows
+
+// Block (i, y): if cut i + 1 is the first inside its item, the parts of that
+// item: the last segment of run i, then the first segments of the runs behind.
+template <int D>
+__global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeAttnParams p, int W)
+{
+    constexpr int E = D / 32;
+    __shared__ int s_slot[kMaxTreeRuns];
+    __shared__ float2 s_w[kCombineThreads / 32][kMaxTreeRuns];
+    __shared__ int4 s_pos[kMaxTreeRuns + 1];
+    __shared__ int s_n;
+    grid_dependency_wait();
+    const int cut = blockIdx.x + 1;
+    const int4 x = p.pos[cut], a = p.pos[cut - 1];
+    if (x.w == 0 || (a.w != 0 && same_item(a, x))) return;
+    Request r;
+    if (read_request(p, x.x, r) != 1) return;
+    const int first = x.z * 2 * p.tb, ntok = min(2 * p.tb, r.T - first), rows = ntok * p.G;
+    if ((int)blockIdx.y * (kCombineThreads / 32) >= rows) return;
+    for (int c = cut + threadIdx.x; c <= W; c += kCombineThreads) s_pos[c] = p.pos[c];
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        int n = 0;
+        s_slot[n++] = 2 * (cut - 1) + 1;
+        int4 at = x;
+        for (int c = cut; c < W && at.w != 0 && same_item(at, x); ++c) {
+            const int4 to = s_pos[c + 1];
+            if (before(at, to)) s_slot[n++] = 2 * c;
+            at = to;
+        }
+        s_n = n;
     }
     __syncthreads();
-    for (int x = tid; x < p.G * D; x += kTreeWarps * 32) {
-        const int g = x / D, c = x - g * D;
-        float mx = -INFINITY, sum = 0.f, acc = 0.f;
-        for (int w = 0; w < kTreeWarps; ++w) mx = fmaxf(mx, s_m[w][g]);
-        for (int w = 0; w < kTreeWarps; ++w) {
-            const float f = s_m[w][g] == -INFINITY ? 0.f : exp2f(s_m[w][g] - mx);
-            sum += s_l[w][g] * f;
-            acc += s_o[w][g][c] * f;
+    const int n = s_n, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int q = blockIdx.y * (kCombineThreads / 32) + warp; q < rows; q += kCombineGroups * (kCombineThreads / 32)) {
+        const int tok = q / p.G, g = q - tok * p.G, half = ntok > p.tb && tok >= p.tb ? 1 : 0;
+        const int row = half * kTRows + (tok - half * p.tb) * p.G + g;
+        float m = -INFINITY;
+        for (int c = lane; c < n; c += 32) {
+            const float2 ml = p.part_ml[(size_t)s_slot[c] * 2 * kTRows + row];
+            s_w[warp][c] = ml;
+            m = fmaxf(m, ml.x);
         }
-        p.out[((size_t)row * p.Hq + kvh * p.G + g) * D + c] = __float2bfloat16_rn(mx == -INFINITY ? 0.f : acc / sum);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        __syncwarp();
+        float l = 0.f, acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int c = 0; c < n; ++c) {
+            const float2 ml = s_w[warp][c];
+            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+            const float* src = p.part_o + ((size_t)s_slot[c] * 2 * kTRows + row) * D + lane * E;
+            float v[E];
+            if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
+            else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+            l = fmaf(f, ml.y, l);
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+        }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        __nv_bfloat16* dst = p.out + (((size_t)r.row0 + first + tok) * p.Hq + (size_t)x.y * p.G + g) * D + lane * E;
+        if (E == 4)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[E - 2] * inv, acc[E - 1] * inv));
+        else
+            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
+        __syncwarp();
     }
+}
+
+template <int D, bool FP8>
+cudaError_t launch_t(const TreeAttnParams& p, const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                     int runs, cudaStream_t stream)
+{
+    tree_attn_kernel<D, FP8><<<runs, TreeGeo<D, FP8>::THREADS, TreeGeo<D, FP8>::BYTES, stream>>>(tmq, tmk, tmv, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || runs < 2) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(runs - 1), kCombineGroups);
+    cfg.blockDim = dim3(kCombineThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_combine_kernel<D>, p, runs);
+}
+
+template <int D, bool FP8>
+cudaError_t prepare_t()
+{
+    return cudaFuncSetAttribute(tree_attn_kernel<D, FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                TreeGeo<D, FP8>::BYTES);
 }
 
 }  // namespace
 
-cudaError_t launch_tree_attn(const TreeAttnParams& p, int head_dim, bool fp8, cudaStream_t stream)
+cudaError_t tree_attn_prepare(int head_dim, bool fp8)
 {
-    const dim3 grid((unsigned)p.n_tokens, (unsigned)p.Hkv), block(kTreeWarps * 32);
-    if (head_dim == 128) {
-        if (fp8) tree_attn_kernel<128, true><<<grid, block, 0, stream>>>(p);
-        else tree_attn_kernel<128, false><<<grid, block, 0, stream>>>(p);
-    } else {
-        if (fp8) tree_attn_kernel<64, true><<<grid, block, 0, stream>>>(p);
-        else tree_attn_kernel<64, false><<<grid, block, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
+    if (head_dim == 128) return fp8 ? prepare_t<128, true>() : prepare_t<128, false>();
+    return fp8 ? prepare_t<64, true>() : prepare_t<64, false>();
+}
+
+cudaError_t launch_tree_attn(const TreeAttnParams& p, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                             const CUtensorMap& tmv, int head_dim, bool fp8, int runs, cudaStream_t stream)
+{
+    if (head_dim == 128)
+        return fp8 ? launch_t<128, true>(p, tmq, tmk, tmv, runs, stream) : launch_t<128, false>(p, tmq, tmk, tmv, runs, stream);
+    return fp8 ? launch_t<64, true>(p, tmq, tmk, tmv, runs, stream) : launch_t<64, false>(p, tmq, tmk, tmv, runs, stream);
 }
 
 }  // namespace pkv

@@ -61,10 +61,20 @@ struct TreeAttnParams {
     const int32_t* cu_q;
     const uint32_t* tree_mask;
     int* err;
+    float* part_o;                // [2 * runs][256][D] fp32, unnormalised: the parts of items at a run's ends
+    float2* part_ml;              // [2 * runs][256] (m in log2 units, l)
+    int4* pos;                    // [runs + 1] where each run starts: request, kv head, block, tile
     float scale_log2;             // log2(e) / sqrt(d)
     int batch, bt_stride, Hq, Hkv, G, P, num_pages, mask_words, n_tokens;
+    int tb;                       // new tokens in the 128 rows of a stream: 128 / G
 };
-cudaError_t launch_tree_attn(const TreeAttnParams& p, int head_dim, bool fp8, cudaStream_t stream);
+constexpr int kTreeRows = 128;
+constexpr int kMaxTreeRuns = 256; // CTAs of the attention at most
+cudaError_t tree_attn_prepare(int head_dim, bool fp8);
+// runs CTAs (one per SM), then the merge of the items they share.  tmq: q as
+// [n_tokens][Hq][D], boxes of tb tokens, G heads, 64 elements.
+cudaError_t launch_tree_attn(const TreeAttnParams& p, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                             const CUtensorMap& tmv, int head_dim, bool fp8, int runs, cudaStream_t stream);
 
 struct TreeCommitParams {
     void* k_pool;
