@@ -192,78 +192,84 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 
 // ---- softmax of one tile --------------------------------------------------------
 
-__device__ __forceinline__ bool bit(const uint32_t (&vis)[4], int c) { return (vis[c >> 5] >> (c & 31)) & 1u; }
+// Both passes go 32 keys at a time in loops that are not unrolled: unrolled,
+// with and without masks, they were over 64 KB of straight code, and fetching
+// it made every warp of the SM several times slower.
+//
+// f: score scale in log2 units.  E4M3: `scales` of lane k holds the K scale of
+// the tile's page k, of lane 8 + k its V scale; pages are 1 << shift keys.
 
-// Largest scaled score of the row in this tile.  kk: score scale in log2
-// units (E4M3: times the K scale, for every 16 keys).
+// Largest scaled score of the row in this tile.
 template <bool FP8, bool MASKED>
-__device__ __forceinline__ float tile_max(uint32_t scol, const uint32_t (&vis)[4], const float (&kk)[8])
+__device__ __forceinline__ float tile_max(uint32_t scol, const uint32_t (&vis)[4], float f, float scales, int shift)
 {
     float mx = -INFINITY;
-#pragma unroll
-    for (int c0 = 0; c0 < kTKeys; c0 += 64) {
-        uint32_t sa[32], sb[32];
-        tmem_ld32(scol + (uint32_t)c0, sa);
-        tmem_ld32(scol + (uint32_t)c0 + 32u, sb);
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        uint32_t x[32];
+        tmem_ld32(scol + (uint32_t)(32 * k), x);
+        const uint32_t see = MASKED ? (k & 2 ? (k & 1 ? vis[3] : vis[2]) : (k & 1 ? vis[1] : vis[0])) : 0u;
         tmem_wait_ld();
+        float g[2] = {-INFINITY, -INFINITY};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {              // 16 keys at a time
-            float g = -INFINITY;
-#pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const float x = __uint_as_float(k < 2 ? sa[16 * k + c] : sb[16 * (k - 2) + c]);
-                g = fmaxf(g, !MASKED || bit(vis, c0 + 16 * k + c) ? x : -INFINITY);
-            }
-            mx = fmaxf(mx, FP8 ? g * kk[c0 / 16 + k] : g);
+        for (int c = 0; c < 32; ++c) {
+            const float v = __uint_as_float(x[c]);
+            g[c >> 4] = fmaxf(g[c >> 4], !MASKED || ((see >> c) & 1u) ? v : -INFINITY);
         }
+        if (FP8) {
+            g[0] *= __shfl_sync(0xffffffffu, scales, (32 * k) >> shift);
+            g[1] *= __shfl_sync(0xffffffffu, scales, (32 * k + 16) >> shift);
+        }
+        mx = fmaxf(mx, fmaxf(g[0], g[1]));
     }
-    return FP8 ? mx : mx * kk[0];
+    return mx * f;
 }
 
 // P = 2^(s - m) over the row's S columns as P_hi + P_lo, 32 keys at a time:
 // keys c0 + 2i, + 1 in column c0 + i (P_hi) and c0 + 16 + i (P_lo).  E4M3: P
 // times the V scale.  Returns the sum of the weights.
 template <bool FP8, bool MASKED>
-__device__ __forceinline__ float tile_weights(uint32_t scol, const uint32_t (&vis)[4], const float (&kk)[8],
-                                              const float (&vs)[8], float m)
+__device__ __forceinline__ float tile_weights(uint32_t scol, const uint32_t (&vis)[4], float f, float scales, int shift,
+                                              float m)
 {
     float sum0 = 0.f, sum1 = 0.f;
-    uint32_t sv[2][32];
-    tmem_ld32(scol, sv[0]);
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t col = scol + (uint32_t)(32 * k);
+        uint32_t x[32];
+        tmem_ld32(col, x);
+        const uint32_t see = MASKED ? (k & 2 ? (k & 1 ? vis[3] : vis[2]) : (k & 1 ? vis[1] : vis[0])) : 0u;
+        float fs[2] = {f, f}, vs[2] = {1.f, 1.f};
+        if (FP8) {
 #pragma unroll
-    for (int k32 = 0; k32 < 4; ++k32) {
-        const int c0 = 32 * k32;
+            for (int h = 0; h < 2; ++h) {
+                fs[h] *= __shfl_sync(0xffffffffu, scales, (32 * k + 16 * h) >> shift);
+                vs[h] = __shfl_sync(0xffffffffu, scales, 8 + ((32 * k + 16 * h) >> shift));
+            }
+        }
         tmem_wait_ld();
-        if (k32 < 3) tmem_ld32(scol + (uint32_t)c0 + 32u, sv[(k32 + 1) & 1]);
-        uint32_t(&s)[32] = sv[k32 & 1];
 #pragma unroll
-        for (int k16 = 0; k16 < 2; ++k16) {
-            const float f = FP8 ? kk[2 * k32 + k16] : kk[0];
+        for (int h = 0; h < 2; ++h) {
             uint32_t hi[8], lo[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const int c = 16 * k16 + 2 * i;
-                float p0 = ex2(fmaf(__uint_as_float(s[c]), f, -m));
-                float p1 = ex2(fmaf(__uint_as_float(s[c + 1]), f, -m));
-                if (MASKED) {
-                    p0 = bit(vis, c0 + c) ? p0 : 0.f;
-                    p1 = bit(vis, c0 + c + 1) ? p1 : 0.f;
-                }
+                const int c = 16 * h + 2 * i;
+                const bool see0 = !MASKED || ((see >> c) & 1u), see1 = !MASKED || ((see >> (c + 1)) & 1u);
+                float p0 = ex2(fmaf(__uint_as_float(x[c]), fs[h], -m));
+                float p1 = ex2(fmaf(__uint_as_float(x[c + 1]), fs[h], -m));
+                p0 = see0 ? p0 : 0.f;
+                p1 = see1 ? p1 : 0.f;
                 sum0 += p0;
                 sum1 += p1;
-                if (FP8) {
-                    p0 *= vs[2 * k32 + k16];
-                    p1 *= vs[2 * k32 + k16];
-                    if (MASKED) {          // 0 x a scale that is no number
-                        p0 = bit(vis, c0 + c) ? p0 : 0.f;
-                        p1 = bit(vis, c0 + c + 1) ? p1 : 0.f;
-                    }
+                if (FP8) {          // selected again: 0 x a scale that is no number
+                    p0 = see0 ? p0 * vs[h] : 0.f;
+                    p1 = see1 ? p1 * vs[h] : 0.f;
                 }
                 hi[i] = pack_bf16(p0, p1);
                 lo[i] = pack_bf16(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
             }
-            tmem_st8(scol + (uint32_t)(c0 + 8 * k16), hi);
-            tmem_st8(scol + (uint32_t)(c0 + 16 + 8 * k16), lo);
+            tmem_st8(col + (uint32_t)(8 * h), hi);
+            tmem_st8(col + (uint32_t)(16 + 8 * h), lo);
         }
     }
     return sum0 + sum1;
@@ -423,12 +429,15 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const int np = __popc(__ballot_sync(0xffffffffu, have));
                 if (lane == 0) mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
                 __syncwarp();
-                if (have) {
-                    const uint32_t dst = dst0 + (uint32_t)(j * LSLOT + lane * p.P * (FP8 ? D : 128));
-                    const int y = (page * p.Hkv + s.kvh) * p.P;
+                for (int i = 0; i < np; ++i) {               // page by page from one thread: the lanes' own would be issued one by one as well
+                    const int y = (__shfl_sync(0xffffffffu, page, i) * p.Hkv + s.kvh) * p.P;
+                    const uint32_t dst = dst0 + (uint32_t)(j * LSLOT + i * p.P * (FP8 ? D : 128));
+                    if (elect_one()) {
 #pragma unroll
-                    for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * LBLK), map, 64 * kb, y, lfull + 8u * j);
+                        for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * LBLK), map, 64 * kb, y, lfull + 8u * j);
+                    }
                 }
+                __syncwarp();
                 ++ld;
             };
             auto load_q = [&](int buf, int& count, int token) {
@@ -477,68 +486,79 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             if (qc1 > 0) (void)mbar_wait_bounded(qfull + 8u, (uint32_t)((qc1 - 1) & 1), kTWaitNs);
         }
     } else if (warp == 1) {
-        // ---- MMA issue, one thread
-        if (lane == 0) {
-            constexpr uint32_t idS = umma_idesc_bf16<kTRows, kTKeys>();
-            constexpr uint32_t idO = umma_idesc_bf16<kTRows, D, true>();
-            int rb = 0, qsel = 0;
-            int qc[2] = {0, 0}, pc[2] = {0, 0};
-            bool ok = true;
-            auto wait = [&](uint32_t bar, int phase) {
-                ok = ok && mbar_wait_bounded(bar, (uint32_t)(phase & 1), kTWaitNs);
-            };
-            while (ok && walk.next(p, s)) {
-                auto score = [&](int u) {
-                    const int st = u & 1, i = s.row_mode ? u >> 1 : u;
-                    const int seq = rb + k_seq(s, i), slot = seq % NS;
-                    const int qb = s.row_mode ? st : qsel;
-                    if (u == 0 || (u == 1 && s.row_mode)) wait(qfull + 8u * qb, qc[qb]++);
-                    wait(full + 8u * slot, seq / NS);
-                    if (!ok) return;
-                    tmem_fence_after();
-                    const uint32_t qa = q0 + (uint32_t)(qb * SLOT), ka = ring + (uint32_t)(slot * SLOT);
+        // ---- MMA issue: the warp together, one elected lane for each instruction
+        constexpr uint32_t idS = umma_idesc_bf16<kTRows, kTKeys>();
+        constexpr uint32_t idO = umma_idesc_bf16<kTRows, D, true>();
+        int rb = 0, qsel = 0, qc0 = 0, qc1 = 0, pc0 = 0, pc1 = 0;
+        bool ok = true;
+        auto wait = [&](uint32_t bar, int phase) {
+            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)(phase & 1), kTWaitNs)) != 0;
+        };
+        auto commit = [&](uint32_t bar) {
+            if (elect_one()) umma_commit(bar);
+        };
+        while (ok && walk.next(p, s)) {
+            auto score = [&](int u) {
+                const int st = u & 1, i = s.row_mode ? u >> 1 : u;
+                const int seq = rb + k_seq(s, i), slot = seq % NS;
+                const int qb = s.row_mode ? st : qsel;
+                if (u == 0 || (u == 1 && s.row_mode)) {
+                    wait(qfull + 8u * qb, qb ? qc1 : qc0);
+                    if (qb) ++qc1;
+                    else ++qc0;
+                }
+                wait(full + 8u * slot, seq / NS);
+                if (!ok) return;
+                tmem_fence_after();
+                const uint64_t qa = sw128_kmajor_desc(q0 + (uint32_t)(qb * SLOT)),
+                               ka = sw128_kmajor_desc(ring + (uint32_t)(slot * SLOT));
+                const uint32_t dcol = tmem + (uint32_t)(st * kTKeys);
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t off = (uint32_t)((kk >> 2) * kTBlk + (kk & 3) * 32);
-                        umma_bf16(tmem + (uint32_t)(st * kTKeys), sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off),
-                                  idS, kk ? 1u : 0u);
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kTBlk + (kk & 3) * 32) >> 4);
+                        umma_bf16_all(dcol, qa + off, ka + off, idS, kk ? 1u : 0u);
                     }
-                    umma_commit(sfull + 8u * st);
-                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
-                    if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) umma_commit(qempty + 8u * qb);
-                };
-                auto values = [&](int u) {
-                    const int st = u & 1, i = s.row_mode ? u >> 1 : u;
-                    const int seq = rb + v_seq(s, i), slot = seq % NS;
-                    wait(pfull + 8u * st, pc[st]++);
-                    wait(full + 8u * slot, seq / NS);
-                    if (!ok) return;
-                    tmem_fence_after();
-                    const uint32_t va = ring + (uint32_t)(slot * SLOT);
-                    const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
+                }
+                commit(sfull + 8u * st);
+                if (!s.row_mode || st) commit(empty + 8u * slot);
+                if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) commit(qempty + 8u * qb);
+            };
+            auto values = [&](int u) {
+                const int st = u & 1, i = s.row_mode ? u >> 1 : u;
+                const int seq = rb + v_seq(s, i), slot = seq % NS;
+                wait(pfull + 8u * st, st ? pc1 : pc0);
+                if (st) ++pc1;
+                else ++pc0;
+                wait(full + 8u * slot, seq / NS);
+                if (!ok) return;
+                tmem_fence_after();
+                const uint64_t va = sw128_mnmajor_desc(ring + (uint32_t)(slot * SLOT), (uint32_t)kTBlk, 1024u);
+                const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
+                const uint32_t later = u >= 2 ? 1u : 0u;
+                if (elect_one()) {
 #pragma unroll
                     for (int kk = 0; kk < 2 * kTKeys / 16; ++kk) {      // 16 keys each: P_hi, then P_lo
                         const int k8 = kk & 7;
-                        umma_bf16_ts(ocol, pcol + (uint32_t)((k8 >> 1) * 32 + (k8 & 1) * 8 + (kk >> 3) * 16),
-                                     sw128_mnmajor_desc(va + (uint32_t)(k8 * 2048), (uint32_t)kTBlk, 1024u), idO,
-                                     (kk || u >= 2) ? 1u : 0u);
+                        umma_bf16_ts_all(ocol, pcol + (uint32_t)((k8 >> 1) * 32 + (k8 & 1) * 8 + (kk >> 3) * 16),
+                                         va + (uint64_t)(k8 * 128), idO, kk ? 1u : later);
                     }
-                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
-                    if (u >= s.units - 2) umma_commit(ofin + 8u * st);
-                };
-                score(0);
-                if (s.units > 1) score(1);
-                for (int u = 0; ok && u < s.units; ++u) {
-                    values(u);
-                    if (u + 2 < s.units) score(u + 2);
                 }
-                if (!s.row_mode) qsel ^= 1;
-                rb += 2 * s.n;
+                if (!s.row_mode || st) commit(empty + 8u * slot);
+                if (u >= s.units - 2) commit(ofin + 8u * st);
+            };
+            score(0);
+            if (s.units > 1) score(1);
+            for (int u = 0; ok && u < s.units; ++u) {
+                values(u);
+                if (u + 2 < s.units) score(u + 2);
             }
-            if (!ok) s_fail = 1;
-            umma_commit(drain);              // every MMA has ended before the tensor memory is given back
-            (void)mbar_wait_bounded(drain, 0u, kTWaitNs);
+            if (!s.row_mode) qsel ^= 1;
+            rb += 2 * s.n;
         }
+        if (!ok) s_fail = 1;
+        commit(drain);                   // every MMA has ended before the tensor memory is given back
+        (void)mbar_wait_bounded(drain, 0u, kTWaitNs);
         __syncwarp();
     } else if (warp < 10) {
         // ---- softmax and output: row r of stream st
@@ -587,18 +607,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             float m = -INFINITY, l = 0.f;
             for (int u = st; u < s.units; u += 2) {
                 const int i = s.row_mode ? u >> 1 : u, key0 = (s.t0 + i) * kTKeys;
-                float kk[8], vs[8];
+                float scales = 0.f;
                 if (FP8) {
-                    const float cur = scale_next;
+                    scales = scale_next;
                     scale_next = scale_of(page_next);
                     page_next = page_of(i + 2 * step);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        kk[k] = __shfl_sync(0xffffffffu, cur, (16 * k) >> shift) * p.scale_log2;
-                        vs[k] = __shfl_sync(0xffffffffu, cur, 8 + ((16 * k) >> shift));
-                    }
-                } else {
-                    kk[0] = p.scale_log2;
                 }
                 wait(sfull + 8u * st, sc++);
                 tmem_fence_after();
@@ -621,13 +634,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                                     if (((32 * w + c) >> shift) == k) vis[w] &= ~(1u << c);
                         }
                     }
-                    const float mx = tail || bad ? tile_max<FP8, true>(scol, vis, kk) : tile_max<FP8, false>(scol, vis, kk);
+                    const float mx = tail || bad ? tile_max<FP8, true>(scol, vis, p.scale_log2, scales, shift)
+                                                : tile_max<FP8, false>(scol, vis, p.scale_log2, scales, shift);
                     if (u < 2) {
                         m = mx;
                     } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
                         // S of this tile was issued after the last P V of the stream: O is settled
                         const float mn = fmaxf(m, mx), alpha = m == mn ? 1.f : ex2(m - mn);
-#pragma unroll
+#pragma unroll 1
                         for (int c0 = 0; c0 < D; c0 += 32) {
                             uint32_t o[32];
                             const uint32_t oc = lanes + kTOcol + (uint32_t)(st * 128 + c0);
@@ -642,8 +656,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                         m = mn;
                     }
                     const float mref = m == -INFINITY ? 0.f : m;
-                    l += tail || bad ? tile_weights<FP8, true>(scol, vis, kk, vs, mref)
-                                     : tile_weights<FP8, false>(scol, vis, kk, vs, mref);
+                    l += tail || bad ? tile_weights<FP8, true>(scol, vis, p.scale_log2, scales, shift, mref)
+                                     : tile_weights<FP8, false>(scol, vis, p.scale_log2, scales, shift, mref);
                     tmem_wait_st();
                 }
                 if (tail && (!s.row_mode || st == 0)) {
@@ -727,6 +741,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const size_t slot_row = ((size_t)(2 * cta + (s.place == 1)) * 2 * kTRows) + (s.row_mode ? st * kTRows : 0) + r;
                 __nv_bfloat16* const orow = p.out + (trow * p.Hq + (size_t)s.kvh * p.G + g) * D;
                 if (valid && s.place && (s.row_mode || st == 0)) p.part_ml[slot_row] = make_float2(m, l);
+#pragma unroll 1
                 for (int c0 = col0; c0 < col0 + cols; c0 += 32) {
                     uint32_t x0[32];
                     float o[32];
