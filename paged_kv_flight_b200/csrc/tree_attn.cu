@@ -11,8 +11,7 @@
 // Mathematics: o = softmax(q K^T / sqrt(d)) V over the keys a row sees, all
 // cached keys and those drafted ones whose mask bit is set.  One pass with a
 // running reference m and sum l per row: S = Q K^T, P = 2^(s - m), l += P,
-// O += P V; a row's m moves only when its maximum passes it by more than 2^8,
-// then O and l are rescaled in place.
+// O += P V; m moves only when the row's maximum passes it by more than 2^8.
 //
 // Work item: a request, one of its kv heads and a block of up to 2 (128 / G)
 // of its new tokens; the G heads of the group times the tokens are the rows
@@ -28,12 +27,12 @@
 // unnormalised O, m and l go to the workspace and are merged by tree_combine
 // in a fixed order.  Nothing waits for another CTA.
 //
-// Warps: 0 loads (TMA), 1 issues the MMAs, 2 .. 9 softmax and output, one
-// thread per row; for E4M3 pools 10 .. 13 turn the codes into bf16 tiles
+// Warps: 0 loads Q and K (TMA), the last one V, 1 issues the MMAs, 2 .. 9
+// softmax and output, one thread per row; for E4M3 pools 10 .. 13 turn the codes into bf16 tiles
 // (exact; the scales of a page and head go into the scores and the weights in
-// fp32).  P goes to the MMA as two bf16 terms P_hi + P_lo (about 16
-// significant bits), so that a row with few keys carries no error of bf16's
-// size beyond its own rounding.
+// fp32).  P is rounded to bf16 for the matrix product, each weight off by at
+// most 2^-8 of itself; two terms of bf16 would cost half as much again on the
+// tensor pipe, which bounds the large trees.
 #include "tree_params.h"
 #include "pkv_device.cuh"
 #include "umma.cuh"
@@ -48,6 +47,7 @@ constexpr int kTKeys = 128;                   // keys of a tile
 constexpr int kTBlk = kTRows * 128;           // 64 columns of a 128-row tile in bf16: 16 KB
 constexpr uint32_t kTCols = 512;              // tensor memory: S / P of two streams, O of two streams
 constexpr uint32_t kTOcol = 2 * kTKeys;
+constexpr int kMaxSlots = 8;
 constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // Relative cost of a tile for the cut: in row mode it has twice the softmax
 // and MMA work of key mode on the same bytes.
@@ -61,9 +61,18 @@ struct TreeGeo {
     static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
     static constexpr int NC = FP8 ? (D == 128 ? 4 : 6) : 0;          // tiles of codes
     static constexpr int STG = kTKeys * D;
-    static constexpr int THREADS = 64 + 256 + (FP8 ? 128 : 0);
+    static constexpr int THREADS = 64 + 256 + (FP8 ? 128 : 0) + 32;
     static constexpr int BYTES = (2 + NS) * SLOT + NC * STG + 1024;
 };
+
+// A bounded wait whose clock starts late: most waits here end within some
+// polls, and reading the timer first costs as much as one of them.
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity)
+{
+    for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_bounded(bar, parity, kTWaitNs);
+}
 
 // ---- the cut ------------------------------------------------------------------
 
@@ -110,6 +119,13 @@ __device__ __forceinline__ bool before(const int4& a, const int4& b)
 }
 __device__ __forceinline__ bool same_item(const int4& a, const int4& b) { return a.x == b.x && a.y == b.y && a.z == b.z; }
 
+// a / b of numbers that are not negative: 64-bit division is called only
+// where it is needed.
+__device__ __forceinline__ long long quotient(long long a, long long b)
+{
+    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+
 __device__ __forceinline__ int4 next_item(int b, int kvh, int blk, int blocks, int Hkv)
 {
     if (++blk < blocks) return make_int4(b, kvh, blk, 0);
@@ -124,11 +140,11 @@ __device__ __forceinline__ int4 place_at(const TreeAttnParams& p, int b, const R
     int rb, nb;
     blocks_of(p, r.T, rb, nb);
     const long long row_cost = (long long)r.NT * kCostRow, head = row_cost * rb + (long long)(nb - rb) * r.NT * kCostKey;
-    const int kvh = (int)(at / head);
+    const int kvh = (int)quotient(at, head);
     at -= head * kvh;
-    const int blk = (int)min(at / row_cost, (long long)rb);
+    const int blk = (int)min(quotient(at, row_cost), (long long)rb);
     at -= row_cost * blk;
-    const int tile = (int)(at / (blk < rb ? kCostRow : kCostKey));
+    const int tile = (int)quotient(at, blk < rb ? kCostRow : kCostKey);
     if (tile <= kSnap) return make_int4(b, kvh, blk, 0);
     if (r.NT - tile <= kSnap) return next_item(b, kvh, blk, nb, p.Hkv);
     return make_int4(b, kvh, blk, tile);
@@ -192,87 +208,128 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 
 // ---- softmax of one tile --------------------------------------------------------
 
-// Both passes go 32 keys at a time in loops that are not unrolled: unrolled,
-// with and without masks, they were over 64 KB of straight code, and fetching
-// it made every warp of the SM several times slower.
+// The scores of keys that the row does not see become -inf, whatever they
+// were (of tiles with drafted keys, or pages out of range, before the pass
+// below: masks in that pass would double its code for one tile in many).
+__device__ __forceinline__ void tile_mask(uint32_t scol, const uint32_t (&vis)[4])
+{
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) {
+        uint32_t x[4][8];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld8(scol + (uint32_t)(32 * k + 8 * c), x[c]);
+        const uint32_t see = k & 2 ? (k & 1 ? vis[3] : vis[2]) : (k & 1 ? vis[1] : vis[0]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int c = 0; c < 32; ++c) x[c >> 3][c & 7] = (see >> c) & 1u ? x[c >> 3][c & 7] : 0xFF800000u;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_st8(scol + (uint32_t)(32 * k + 8 * c), x[c]);
+    }
+    tmem_wait_st();
+}
+
+// 16 columns of this lane times alpha: fp32, or pairs of bf16 (exact for a
+// power of two).
+template <bool BF16>
+__device__ __forceinline__ void tmem_scale16(uint32_t col, float alpha)
+{
+    uint32_t x[2][8];
+    tmem_ld8(col, x[0]);
+    tmem_ld8(col + 8u, x[1]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c)
+            x[h][c] = BF16 ? pack_bf16(bf16_lo(x[h][c]) * alpha, bf16_hi(x[h][c]) * alpha)
+                           : __float_as_uint(__uint_as_float(x[h][c]) * alpha);
+        tmem_st8(col + (uint32_t)(8 * h), x[h]);
+    }
+}
+
+// One pass over the row's S, 64 keys (E4M3: 32) at a time in a loop that is not unrolled
+// (unrolled, the code was over 64 KB, and fetching it made every warp of the SM
+// several times slower).  A chunk's maximum is taken
+// while its scores are in registers; the reference m, a whole number, moves
+// only when some row of the warp passes it by more than 2^8, and then what was
+// made with the old one (O of this stream, the tile's chunks of P, l) is
+// multiplied by a power of two, which is exact.  P = 2^(s - m) goes back as
+// bf16 over the S columns already read, keys 2i and 2i + 1 in column i.
 //
 // f: score scale in log2 units.  E4M3: `scales` of lane k holds the K scale of
 // the tile's page k, of lane 8 + k its V scale; pages are 1 << shift keys.
-
-// Largest scaled score of the row in this tile.
-template <bool FP8, bool MASKED>
-__device__ __forceinline__ float tile_max(uint32_t scol, const uint32_t (&vis)[4], float f, float scales, int shift)
+template <int D, bool FP8>
+__device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool first, float f, float scales, int shift,
+                                             float& m, float& l)
 {
-    float mx = -INFINITY;
+    constexpr int N = FP8 ? 32 : 64;                          // keys of a chunk
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-        uint32_t x[32];
-        tmem_ld32(scol + (uint32_t)(32 * k), x);
-        const uint32_t see = MASKED ? (k & 2 ? (k & 1 ? vis[3] : vis[2]) : (k & 1 ? vis[1] : vis[0])) : 0u;
-        tmem_wait_ld();
-        float g[2] = {-INFINITY, -INFINITY};
+    for (int k = 0; k < kTKeys / N; ++k) {
+        uint32_t x[N];
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-            const float v = __uint_as_float(x[c]);
-            g[c >> 4] = fmaxf(g[c >> 4], !MASKED || ((see >> c) & 1u) ? v : -INFINITY);
-        }
-        if (FP8) {
-            g[0] *= __shfl_sync(0xffffffffu, scales, (32 * k) >> shift);
-            g[1] *= __shfl_sync(0xffffffffu, scales, (32 * k + 16) >> shift);
-        }
-        mx = fmaxf(mx, fmaxf(g[0], g[1]));
-    }
-    return mx * f;
-}
-
-// P = 2^(s - m) over the row's S columns as P_hi + P_lo, 32 keys at a time:
-// keys c0 + 2i, + 1 in column c0 + i (P_hi) and c0 + 16 + i (P_lo).  E4M3: P
-// times the V scale.  Returns the sum of the weights.
-template <bool FP8, bool MASKED>
-__device__ __forceinline__ float tile_weights(uint32_t scol, const uint32_t (&vis)[4], float f, float scales, int shift,
-                                              float m)
-{
-    float sum0 = 0.f, sum1 = 0.f;
-#pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-        const uint32_t col = scol + (uint32_t)(32 * k);
-        uint32_t x[32];
-        tmem_ld32(col, x);
-        const uint32_t see = MASKED ? (k & 2 ? (k & 1 ? vis[3] : vis[2]) : (k & 1 ? vis[1] : vis[0])) : 0u;
-        float fs[2] = {f, f}, vs[2] = {1.f, 1.f};
+        for (int c = 0; c < N; c += 32) tmem_ld32(scol + (uint32_t)(N * k + c), *reinterpret_cast<uint32_t(*)[32]>(&x[c]));
+        float fs[N / 16], vs[N / 16];
         if (FP8) {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                fs[h] *= __shfl_sync(0xffffffffu, scales, (32 * k + 16 * h) >> shift);
-                vs[h] = __shfl_sync(0xffffffffu, scales, 8 + ((32 * k + 16 * h) >> shift));
+            for (int h = 0; h < N / 16; ++h) {
+                fs[h] = f * __shfl_sync(0xffffffffu, scales, (N * k + 16 * h) >> shift);
+                vs[h] = __shfl_sync(0xffffffffu, scales, 8 + ((N * k + 16 * h) >> shift));
             }
         }
         tmem_wait_ld();
+        float g[N / 16][4];                                    // short chains: one warp alone has to fill its pipes
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t hi[8], lo[8];
+        for (int c = 0; c < N; ++c) {
+            const float v = __uint_as_float(x[c]);
+            float& y = g[c >> 4][c & 3];
+            y = (c & 15) < 4 ? v : fmaxf(y, v);
+        }
+        float mx = -INFINITY;
+#pragma unroll
+        for (int h = 0; h < N / 16; ++h) {
+            const float y = fmaxf(fmaxf(g[h][0], g[h][1]), fmaxf(g[h][2], g[h][3]));
+            mx = fmaxf(mx, FP8 ? y * fs[h] : y);
+        }
+        if (!FP8) mx *= f;
+        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+            const float mn = fmaxf(m, ceilf(mx)), alpha = m == mn ? 1.f : ex2(m - mn);
+            if (!first) {          // S of this tile was issued after the last P V of the stream: O is settled
+#pragma unroll 1
+                for (int c0 = 0; c0 < D; c0 += 16) tmem_scale16<false>(ocol + (uint32_t)c0, alpha);
+            }
+            tmem_wait_st();
+#pragma unroll 1
+            for (int c0 = 0; c0 < N / 2 * k; c0 += 16) tmem_scale16<true>(scol + (uint32_t)c0, alpha);
+            l *= alpha;
+            m = mn;
+        }
+        const float mref = m == -INFINITY ? 0.f : m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < N / 16; ++h) {                     // 16 keys: 8 columns
+            uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = 16 * h + 2 * i;
-                const bool see0 = !MASKED || ((see >> c) & 1u), see1 = !MASKED || ((see >> (c + 1)) & 1u);
-                float p0 = ex2(fmaf(__uint_as_float(x[c]), fs[h], -m));
-                float p1 = ex2(fmaf(__uint_as_float(x[c + 1]), fs[h], -m));
-                p0 = see0 ? p0 : 0.f;
-                p1 = see1 ? p1 : 0.f;
-                sum0 += p0;
-                sum1 += p1;
-                if (FP8) {          // selected again: 0 x a scale that is no number
-                    p0 = see0 ? p0 * vs[h] : 0.f;
-                    p1 = see1 ? p1 * vs[h] : 0.f;
+                float p0 = ex2(fmaf(__uint_as_float(x[c]), FP8 ? fs[h] : f, -mref));
+                float p1 = ex2(fmaf(__uint_as_float(x[c + 1]), FP8 ? fs[h] : f, -mref));
+                if (FP8) {          // the V scale goes into the weights that P V takes, not into their sum
+                    sum[2 * (i & 1)] += p0;
+                    sum[2 * (i & 1) + 1] += p1;
+                    p0 *= vs[h];
+                    p1 *= vs[h];
+                    w[i] = pack_bf16(p0, p1);
+                } else {            // the sum of what P V takes: the weights add up to what divides them
+                    w[i] = pack_bf16(p0, p1);
+                    sum[2 * (i & 1)] += bf16_lo(w[i]);
+                    sum[2 * (i & 1) + 1] += bf16_hi(w[i]);
                 }
-                hi[i] = pack_bf16(p0, p1);
-                lo[i] = pack_bf16(p0 - bf16_lo(hi[i]), p1 - bf16_hi(hi[i]));
             }
-            tmem_st8(col + (uint32_t)(8 * h), hi);
-            tmem_st8(col + (uint32_t)(16 + 8 * h), lo);
+            tmem_st8(scol + (uint32_t)(N / 2 * k + 8 * h), w);
         }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
     }
-    return sum0 + sum1;
+    tmem_wait_st();
 }
 
 // ---- the kernel -------------------------------------------------------------------
@@ -293,6 +350,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
     __shared__ int4 s_pos[2];
     __shared__ uint32_t s_tmem;
     __shared__ int s_bad, s_fail, s_odd;
+    __shared__ int s_issued[kMaxSlots + 2];       // loads issued into each slot, and of each Q
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int cta = blockIdx.x, W = gridDim.x;
@@ -304,6 +362,34 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                    cempty = smem_u32(s_cempty), qfull = smem_u32(s_qfull), qempty = smem_u32(s_qempty),
                    sfull = smem_u32(s_sfull), pfull = smem_u32(s_pfull), ofin = smem_u32(s_ofin),
                    drain = smem_u32(&s_drain);
+
+    // ---- set up, while the lengths are read
+    if (tid == 0) {
+        s_bad = 0;
+        s_fail = 0;
+        s_odd = 0;
+        for (int i = 0; i < kMaxSlots + 2; ++i) s_issued[i] = 0;
+        prefetch_tensormap(&tmq);
+        prefetch_tensormap(&tmk);
+        prefetch_tensormap(&tmv);
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(full + 8u * i, FP8 ? 4u : 1u);
+            mbar_init(empty + 8u * i, 1u);
+        }
+        for (int i = 0; FP8 && i < NCX; ++i) {
+            mbar_init(cfull + 8u * i, 1u);
+            mbar_init(cempty + 8u * i, 4u);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(qfull + 8u * i, 1u);
+            mbar_init(qempty + 8u * i, 1u);
+            mbar_init(sfull + 8u * i, 1u);
+            mbar_init(pfull + 8u * i, 4u);
+            mbar_init(ofin + 8u * i, 1u);
+        }
+        mbar_init(drain, 1u);
+        fence_mbar_init();
+    }
 
     // ---- where this CTA's run starts and ends
     {
@@ -333,7 +419,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             total += s_scan[w];
         }
         for (int k = 0; k < 2; ++k) {
-            const long long x = total * (cta + k) / W;
+            const long long x = quotient(total * (cta + k), W);
             if (x < pre || x >= pre + mine) continue;
             long long at = pre;
             for (int b = lo; b < hi; ++b) {
@@ -361,31 +447,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
     walk.end = s_pos[1];
     if (!before(walk.cur, walk.end)) return;      // the whole CTA
 
-    if (tid == 0) {
-        s_bad = 0;
-        s_fail = 0;
-        s_odd = 0;
-        prefetch_tensormap(&tmq);
-        prefetch_tensormap(&tmk);
-        prefetch_tensormap(&tmv);
-        for (int i = 0; i < NS; ++i) {
-            mbar_init(full + 8u * i, FP8 ? 4u : 1u);
-            mbar_init(empty + 8u * i, 1u);
-        }
-        for (int i = 0; FP8 && i < NCX; ++i) {
-            mbar_init(cfull + 8u * i, 1u);
-            mbar_init(cempty + 8u * i, 4u);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(qfull + 8u * i, 1u);
-            mbar_init(qempty + 8u * i, 1u);
-            mbar_init(sfull + 8u * i, 1u);
-            mbar_init(pfull + 8u * i, 4u);
-            mbar_init(ofin + 8u * i, 1u);
-        }
-        mbar_init(drain, 1u);
-        fence_mbar_init();
-    }
     if (warp == 1) {
         __syncwarp();
         tmem_alloc(smem_u32(&s_tmem), kTCols);
@@ -396,16 +457,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
     const uint32_t tmem = s_tmem;
     Segment s;
 
-    if (warp == 0) {
-        // ---- loads
+    if (warp == 0 || warp == WARPS - 1) {
+        // ---- loads: warp 0 those of Q and K, the last warp those of V (a box
+        // takes about 100 cycles to issue; one warp alone was what bounded
+        // pages of 16 tokens)
+        const bool is_v = warp != 0;
+        const CUtensorMap* const map = is_v ? &tmv : &tmk;
         constexpr int N = FP8 ? NCX : NS;
         constexpr int ROWB = FP8 ? D : 2 * D;                // bytes of a row in the pool
         const uint32_t lfull = FP8 ? cfull : full, lempty = FP8 ? cempty : empty, dst0 = FP8 ? stage : ring;
         constexpr int LSLOT = FP8 ? Gm::STG : SLOT;
-        constexpr int LB = FP8 ? 1 : KB, LBLK = kTBlk;       // TMA boxes across a row
+        constexpr int LB = FP8 ? 1 : KB;                     // TMA boxes across a row
         const int ppt = kTKeys / p.P;
-        int ld = 0, qc0 = 0, qc1 = 0, qsel = 0;
+        int rb = 0, qc0 = 0, qc1 = 0, qsel = 0;
         bool ok = true;
+        auto wait = [&](uint32_t bar, int phase) {
+            ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
+        };
         while (ok && walk.next(p, s)) {
             const int n_keys = s.L + s.T;
             const int32_t* bt = p.block_tables + (size_t)s.b * p.bt_stride;
@@ -415,35 +483,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const int page = __ldg(&bt[at]);
                 return (unsigned)page < (unsigned)p.num_pages ? page : -1;
             };
-            int pg0 = page_of(0), pg1 = page_of(1), pg2 = page_of(2);
-            auto load = [&](const CUtensorMap* map, int page) {
-                const int j = ld % N;
-                if (ld >= N) ok = __all_sync(0xffffffffu, mbar_wait_bounded(lempty + 8u * j, (uint32_t)((ld / N - 1) & 1), kTWaitNs));
-                if (!ok) return;
-                const bool have = page != -2;
-                if (page == -1) {
-                    s_bad = 1;                               // its keys are masked; an in-range page keeps the copy legal
-                    atomicOr(p.err, kErrPage);
-                    page = 0;
-                }
-                const int np = __popc(__ballot_sync(0xffffffffu, have));
-                if (lane == 0) mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
-                __syncwarp();
-                for (int i = 0; i < np; ++i) {               // page by page from one thread: the lanes' own would be issued one by one as well
-                    const int y = (__shfl_sync(0xffffffffu, page, i) * p.Hkv + s.kvh) * p.P;
-                    const uint32_t dst = dst0 + (uint32_t)(j * LSLOT + i * p.P * (FP8 ? D : 128));
-                    if (elect_one()) {
-#pragma unroll
-                        for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * LBLK), map, 64 * kb, y, lfull + 8u * j);
-                    }
-                }
-                __syncwarp();
-                ++ld;
-            };
             auto load_q = [&](int buf, int& count, int token) {
-                if (count > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(qempty + 8u * buf, (uint32_t)((count - 1) & 1), kTWaitNs));
+                if (count > 0) wait(qempty + 8u * buf, count - 1);
                 if (!ok) return;
-                if (lane == 0) {
+                if (elect_one()) {
+                    s_issued[kMaxSlots + buf] = count + 1;
                     mbar_arrive_expect_tx(qfull + 8u * buf, (uint32_t)(KB * 128 * p.tb * p.G));
 #pragma unroll
                     for (int kb = 0; kb < KB; ++kb)
@@ -452,20 +496,34 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 __syncwarp();
                 ++count;
             };
-            int ik = 0, iv = 0;
-            const int lead = s.row_mode ? 1 : 2;
-            while (ok && iv < s.n) {
-                if (ik < s.n && ik < iv + lead) {
-                    load(&tmk, ik == iv ? pg0 : pg1);
-                    ++ik;
-                } else {
-                    load(&tmv, pg0);
-                    ++iv;
-                    pg0 = pg1;
-                    pg1 = pg2;
-                    pg2 = page_of(iv + 2);
+            int page = page_of(0);
+            for (int i = 0; ok && i < s.n; ++i) {
+                const int cur = page;
+                page = page_of(i + 1);
+                const int seq = rb + (is_v ? v_seq(s, i) : k_seq(s, i)), j = seq % N;
+                if (seq >= N) wait(lempty + 8u * j, seq / N - 1);
+                if (!ok) break;
+                if (cur == -1) {                             // its keys are masked; an in-range page keeps the copy legal
+                    s_bad = 1;
+                    atomicOr(p.err, kErrPage);
                 }
-                if (ok && ik + iv == 2) {      // the first tiles are under way: now Q, once it is free
+                const int np = __popc(__ballot_sync(0xffffffffu, cur != -2));
+                const int y = (max(cur, 0) * p.Hkv + s.kvh) * p.P;
+                if (elect_one()) {
+                    s_issued[j] = seq / N + 1;
+                    mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
+                }
+                uint32_t dst = dst0 + (uint32_t)(j * LSLOT);
+                for (int k = 0; k < np; ++k) {
+                    const int yk = __shfl_sync(0xffffffffu, y, k);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * kTBlk), map, 64 * kb, yk, lfull + 8u * j);
+                    }
+                    dst += (uint32_t)(p.P * (FP8 ? D : 128));
+                }
+                __syncwarp();
+                if (!is_v && i == 0) {                       // the first tile is under way: now Q, once it is free
                     if (s.row_mode) {
                         load_q(0, qc0, s.row0);
                         load_q(1, qc1, s.row0 + p.tb);
@@ -476,15 +534,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     }
                 }
             }
+            rb += 2 * s.n;
         }
-        if (!ok || *(volatile int*)&s_fail) {
-            // copies under way land before the CTA's memory is given back
-            s_fail = 1;
-            for (int j = max(0, ld - N); j < ld; ++j)
-                (void)mbar_wait_bounded(lfull + 8u * (j % N), (uint32_t)((j / N) & 1), kTWaitNs);
-            if (qc0 > 0) (void)mbar_wait_bounded(qfull, (uint32_t)((qc0 - 1) & 1), kTWaitNs);
-            if (qc1 > 0) (void)mbar_wait_bounded(qfull + 8u, (uint32_t)((qc1 - 1) & 1), kTWaitNs);
-        }
+        if (!ok) s_fail = 1;
     } else if (warp == 1) {
         // ---- MMA issue: the warp together, one elected lane for each instruction
         constexpr uint32_t idS = umma_idesc_bf16<kTRows, kTKeys>();
@@ -492,22 +544,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         int rb = 0, qsel = 0, qc0 = 0, qc1 = 0, pc0 = 0, pc1 = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, int phase) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)(phase & 1), kTWaitNs)) != 0;
-        };
-        auto commit = [&](uint32_t bar) {
-            if (elect_one()) umma_commit(bar);
+            ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
         };
         while (ok && walk.next(p, s)) {
-            auto score = [&](int u) {
-                const int st = u & 1, i = s.row_mode ? u >> 1 : u;
-                const int seq = rb + k_seq(s, i), slot = seq % NS;
-                const int qb = s.row_mode ? st : qsel;
+            // what S(u) reads has landed
+            auto score_ready = [&](int u) {
+                const int i = s.row_mode ? u >> 1 : u, seq = rb + k_seq(s, i);
                 if (u == 0 || (u == 1 && s.row_mode)) {
+                    const int qb = s.row_mode ? u : qsel;
                     wait(qfull + 8u * qb, qb ? qc1 : qc0);
                     if (qb) ++qc1;
                     else ++qc0;
                 }
-                wait(full + 8u * slot, seq / NS);
+                wait(full + 8u * (seq % NS), seq / NS);
+            };
+            auto score = [&](int u) {
+                const int st = u & 1, i = s.row_mode ? u >> 1 : u;
+                const int slot = (rb + k_seq(s, i)) % NS;
+                const int qb = s.row_mode ? st : qsel;
                 if (!ok) return;
                 tmem_fence_after();
                 const uint64_t qa = sw128_kmajor_desc(q0 + (uint32_t)(qb * SLOT)),
@@ -519,18 +573,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                         const uint64_t off = (uint64_t)(((kk >> 2) * kTBlk + (kk & 3) * 32) >> 4);
                         umma_bf16_all(dcol, qa + off, ka + off, idS, kk ? 1u : 0u);
                     }
+                    umma_commit(sfull + 8u * st);
+                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
+                    if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) umma_commit(qempty + 8u * qb);
                 }
-                commit(sfull + 8u * st);
-                if (!s.row_mode || st) commit(empty + 8u * slot);
-                if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) commit(qempty + 8u * qb);
+                __syncwarp();
             };
             auto values = [&](int u) {
                 const int st = u & 1, i = s.row_mode ? u >> 1 : u;
                 const int seq = rb + v_seq(s, i), slot = seq % NS;
+                wait(full + 8u * slot, seq / NS);
                 wait(pfull + 8u * st, st ? pc1 : pc0);
                 if (st) ++pc1;
                 else ++pc0;
-                wait(full + 8u * slot, seq / NS);
                 if (!ok) return;
                 tmem_fence_after();
                 const uint64_t va = sw128_mnmajor_desc(ring + (uint32_t)(slot * SLOT), (uint32_t)kTBlk, 1024u);
@@ -538,26 +593,31 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const uint32_t later = u >= 2 ? 1u : 0u;
                 if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 2 * kTKeys / 16; ++kk) {      // 16 keys each: P_hi, then P_lo
-                        const int k8 = kk & 7;
-                        umma_bf16_ts_all(ocol, pcol + (uint32_t)((k8 >> 1) * 32 + (k8 & 1) * 8 + (kk >> 3) * 16),
-                                         va + (uint64_t)(k8 * 128), idO, kk ? 1u : later);
-                    }
+                    for (int kk = 0; kk < kTKeys / 16; ++kk)            // 16 keys each
+                        umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
+                    if (u >= s.units - 2) umma_commit(ofin + 8u * st);
                 }
-                if (!s.row_mode || st) commit(empty + 8u * slot);
-                if (u >= s.units - 2) commit(ofin + 8u * st);
+                __syncwarp();
             };
+            score_ready(0);
             score(0);
-            if (s.units > 1) score(1);
+            if (s.units > 1) {
+                score_ready(1);
+                score(1);
+            }
             for (int u = 0; ok && u < s.units; ++u) {
                 values(u);
-                if (u + 2 < s.units) score(u + 2);
+                if (u + 2 < s.units) {
+                    score_ready(u + 2);
+                    score(u + 2);
+                }
             }
             if (!s.row_mode) qsel ^= 1;
             rb += 2 * s.n;
         }
         if (!ok) s_fail = 1;
-        commit(drain);                   // every MMA has ended before the tensor memory is given back
+        if (elect_one()) umma_commit(drain);                   // every MMA has ended before the tensor memory is given back
         (void)mbar_wait_bounded(drain, 0u, kTWaitNs);
         __syncwarp();
     } else if (warp < 10) {
@@ -570,7 +630,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         int rb = 0, sc = 0, oc0 = 0, oc1 = 0;
         bool ok = true;
         auto wait = [&](uint32_t bar, int phase) {
-            ok = ok && __all_sync(0xffffffffu, mbar_wait_bounded(bar, (uint32_t)(phase & 1), kTWaitNs)) != 0;
+            ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
         };
         auto pair = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + quarter) : "memory"); };   // the two warps of these lanes
         while (walk.next(p, s)) {
@@ -593,10 +653,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const int at = ((s.t0 + i) << (7 - shift)) + (lane & 7);
                 return FP8 && i < s.n && lane < 16 && at * p.P < n_keys && (lane & 7) < (kTKeys >> shift) ? __ldg(&bt[at]) : -1;
             };
-            auto scale_of = [&](int page) {
-                return FP8 && (unsigned)page < (unsigned)p.num_pages
-                           ? __ldg(&(lane < 8 ? p.k_scale : p.v_scale)[(size_t)page * p.Hkv + s.kvh])
-                           : 0.f;
+            auto scale_of = [&](int page) {      // 1 where there is no page; 0 made tiny: -inf x 0 is no number
+                if (!FP8 || (unsigned)page >= (unsigned)p.num_pages) return 1.f;
+                const float x = __ldg(&(lane < 8 ? p.k_scale : p.v_scale)[(size_t)page * p.Hkv + s.kvh]);
+                return x == 0.f ? 1e-30f : x;
             };
             float scale_next = 0.f;
             int page_next = -1;
@@ -618,8 +678,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const bool bad = *(volatile int*)&s_bad != 0;
                 const bool tail = key0 + kTKeys > s.L;
                 if (ok && act) {
-                    uint32_t vis[4];
                     if (tail || bad) {
+                        uint32_t vis[4];
 #pragma unroll
                         for (int w = 0; w < 4; ++w) {
                             const int d0 = key0 - s.L + 32 * w;
@@ -629,36 +689,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                             const int at = (key0 >> shift) + k;
                             if (at * p.P >= n_keys || (unsigned)__ldg(&bt[at]) < (unsigned)p.num_pages) continue;
 #pragma unroll
-                            for (int w = 0; w < 4; ++w)
-                                for (int c = 0; c < 32; ++c)
-                                    if (((32 * w + c) >> shift) == k) vis[w] &= ~(1u << c);
+                            for (int w = 0; w < 4; ++w) {          // the page's keys: 16 or 32 bits of a word, or two words
+                                const int c = (k << shift) - 32 * w;
+                                if (c > -32 && c < 32) vis[w] &= ~((shift == 4 ? 0xFFFFu : 0xFFFFFFFFu) << max(c, 0));
+                            }
                         }
+                        tile_mask(scol, vis);
                     }
-                    const float mx = tail || bad ? tile_max<FP8, true>(scol, vis, p.scale_log2, scales, shift)
-                                                : tile_max<FP8, false>(scol, vis, p.scale_log2, scales, shift);
-                    if (u < 2) {
-                        m = mx;
-                    } else if (__any_sync(0xffffffffu, mx > m + 8.f)) {
-                        // S of this tile was issued after the last P V of the stream: O is settled
-                        const float mn = fmaxf(m, mx), alpha = m == mn ? 1.f : ex2(m - mn);
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 32) {
-                            uint32_t o[32];
-                            const uint32_t oc = lanes + kTOcol + (uint32_t)(st * 128 + c0);
-                            tmem_ld32(oc, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-#pragma unroll
-                            for (int c = 0; c < 32; c += 8) tmem_st8(oc + (uint32_t)c, *reinterpret_cast<const uint32_t(*)[8]>(&o[c]));
-                        }
-                        l *= alpha;
-                        m = mn;
-                    }
-                    const float mref = m == -INFINITY ? 0.f : m;
-                    l += tail || bad ? tile_weights<FP8, true>(scol, vis, p.scale_log2, scales, shift, mref)
-                                     : tile_weights<FP8, false>(scol, vis, p.scale_log2, scales, shift, mref);
-                    tmem_wait_st();
+                    tile_softmax<D, FP8>(scol, lanes + kTOcol + (uint32_t)(st * 128), u < 2, p.scale_log2, scales, shift, m, l);
                 }
                 if (tail && (!s.row_mode || st == 0)) {
                     // V rows behind the last key hold anything: zero them, so that
@@ -795,7 +833,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             rb += 2 * s.n;
         }
         if (!ok) s_fail = 1;
-    } else if (FP8) {
+    } else if (FP8) {       // warps 10 .. 13
         // ---- codes to bf16: lane l of a warp takes row 8 k + l % 8, 16 codes l / 8 + 4 j
         const int w = warp - 10;
         int q = 0;
@@ -803,9 +841,9 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         while (ok && walk.next(p, s)) {
             for (int e = q + 2 * s.n; ok && q < e; ++q) {
                 const int c = q % NCX, slot = q % NS;
-                ok = __all_sync(0xffffffffu, mbar_wait_bounded(cfull + 8u * c, (uint32_t)((q / NCX) & 1), kTWaitNs)) != 0;
+                ok = __all_sync(0xffffffffu, wait_bar(cfull + 8u * c, (uint32_t)((q / NCX) & 1))) != 0;
                 if (ok && q >= NS)
-                    ok = __all_sync(0xffffffffu, mbar_wait_bounded(empty + 8u * slot, (uint32_t)((q / NS - 1) & 1), kTWaitNs)) != 0;
+                    ok = __all_sync(0xffffffffu, wait_bar(empty + 8u * slot, (uint32_t)((q / NS - 1) & 1))) != 0;
                 if (!ok) break;
                 const uint32_t src = stage + (uint32_t)(c * Gm::STG), dst = ring + (uint32_t)(slot * SLOT);
 #pragma unroll
@@ -847,7 +885,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
     if (warp == 1) {
         __syncwarp();
         tmem_dealloc(tmem, kTCols);
-        if (lane == 0 && s_fail) atomicOr(p.err, kErrTimeout);
+        if (lane == 0 && s_fail) {
+            // copies under way land before the CTA's memory is given back
+            atomicOr(p.err, kErrTimeout);
+            for (int i = 0; i < (FP8 ? NCX : NS); ++i)
+                if (s_issued[i]) (void)mbar_wait_bounded((FP8 ? cfull : full) + 8u * i, (uint32_t)((s_issued[i] - 1) & 1), kTWaitNs);
+            for (int i = 0; i < 2; ++i)
+                if (s_issued[kMaxSlots + i]) (void)mbar_wait_bounded(qfull + 8u * i, (uint32_t)((s_issued[kMaxSlots + i] - 1) & 1), kTWaitNs);
+        }
     }
 }
 

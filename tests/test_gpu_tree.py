@@ -4,10 +4,10 @@ bits (tests/_tree.py) at the sizes and masks where it can go wrong, then the
 four together as a speculative step uses them, eager and captured.
 
 Tolerances, by arithmetic: one rounding to bf16 is off by at most 2^-8 of the
-value.  Attention adds to it 2^-12 of A = sum of weight x |v|: the weights
-carry an error of at most d 2^-23 sqrt(d) ~ 2^-13.6 for the fp32 score sums of
-N(0, 1) data at d = 128, 2^-16 where they are rounded for the matrix product
-and 2^-21 from exp2 and the sums.  Rotation adds 2^-20 (|a| + |b|): an angle
+value.  Attention adds to it 2^-8 + 2^-12 of A = sum of weight x |v|: each
+weight is rounded to bf16 for the matrix product (2^-8 of itself), and carries
+an error of at most d 2^-23 sqrt(d) ~ 2^-13.6 for the fp32 score sums of
+N(0, 1) data at d = 128 and 2^-21 from exp2 and the sums.  Rotation adds 2^-20 (|a| + |b|): an angle
 off by 2^-22 and three fp32 roundings.  E4M3 codes are off by at most 2^-4 of
 the value or half the smallest step, 2^-10 scale."""
 import numpy as np
@@ -18,6 +18,7 @@ from tests import _tree
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
+W = 2.0 ** -8 + 2.0 ** -12      # share of A by which the attention may be off
 
 
 @pytest.fixture(scope="module")
@@ -326,7 +327,7 @@ def _attn_run(pkv, ctx, g, out=None):
 
 def _attn_near(out, ref, size):
     got = _tree.values(out)
-    err = np.abs(got - ref) - (2.0 ** -8 * np.abs(ref) + 2.0 ** -12 * size)
+    err = np.abs(got - ref) - (2.0 ** -8 * np.abs(ref) + W * size)
     assert (err <= 0).all(), (float(np.nanmax(err)), int((~(err <= 0)).sum()))
 
 
@@ -397,7 +398,7 @@ def test_tree_attention_large_scores(pkv):
     with _attn_ctx(pkv, x) as ctx:
         got = _tree.values(_attn_run(pkv, ctx, _attn_device(x)))
         _ok(pkv, ctx)
-    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -12 + s) * size).all()
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + (W + s) * size).all()
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -427,7 +428,7 @@ def test_tree_attention_ignores_what_is_masked(pkv, fp8):
         if r in rows:
             assert not np.isfinite(got[r]).any(), r
         else:
-            assert (np.abs(got[r] - ref[r]) <= 2.0 ** -8 * np.abs(ref[r]) + 2.0 ** -12 * size[r]).all(), r
+            assert (np.abs(got[r] - ref[r]) <= 2.0 ** -8 * np.abs(ref[r]) + W * size[r]).all(), r
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -669,7 +670,7 @@ class _Step:
         # a K or V code next to a border may have been rounded the other way:
         # one step of the type in the new tokens' entries (their share of the weights is below 1)
         step = 2.0 ** -3 if self.fp8 else 2.0 ** -7
-        assert (np.abs(out[:n] - ref) <= 2.0 ** -8 * np.abs(ref) + 2.0 ** -12 * size + step * 0.5 * size).all()
+        assert (np.abs(out[:n] - ref) <= 2.0 ** -8 * np.abs(ref) + W * size + step * 0.5 * size).all()
         # the accepted tokens, where the next step reads them
         lens = self.lens + h["plen"]
         gk = _tree.values(d["k"])
