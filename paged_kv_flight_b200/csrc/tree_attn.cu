@@ -49,9 +49,12 @@ constexpr uint32_t kTCols = 512;              // tensor memory: S / P of two str
 constexpr uint32_t kTOcol = 2 * kTKeys;
 constexpr int kMaxSlots = 8;
 constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
-// Relative cost of a tile for the cut: in row mode it has twice the softmax
-// and MMA work of key mode on the same bytes.
-constexpr int kCostRow = 3, kCostKey = 2;
+// Cost of a tile for the cut, and of an item besides its tiles (Q, the masked
+// tile, the merge of the streams, the output).  Fitted over the CTAs of three
+// workloads: 4758 cycles a tile in row mode, 2450 to 2790 in key mode, 10.6 to
+// 14.2 thousand an item.  Cut by tiles alone, the slowest CTA took 1.5 to 2
+// times the mean.
+constexpr int kCostRow = 4, kCostKey = 2, kCostItem = 9;
 constexpr int kSnap = 2;                      // a cut this near to an item's ends moves there
 
 template <int D, bool FP8>
@@ -109,7 +112,7 @@ __device__ __forceinline__ long long cost_of(const TreeAttnParams& p, const Requ
 {
     int rb, nb;
     blocks_of(p, r.T, rb, nb);
-    return (long long)p.Hkv * r.NT * ((long long)rb * kCostRow + (nb - rb) * kCostKey);
+    return (long long)p.Hkv * (rb * ((long long)r.NT * kCostRow + kCostItem) + (nb - rb) * ((long long)r.NT * kCostKey + kCostItem));
 }
 
 // A place in the order of all tiles: request, kv head, block, tile.
@@ -139,12 +142,13 @@ __device__ __forceinline__ int4 place_at(const TreeAttnParams& p, int b, const R
 {
     int rb, nb;
     blocks_of(p, r.T, rb, nb);
-    const long long row_cost = (long long)r.NT * kCostRow, head = row_cost * rb + (long long)(nb - rb) * r.NT * kCostKey;
+    const long long row_cost = (long long)r.NT * kCostRow + kCostItem,
+                    head = row_cost * rb + (nb - rb) * ((long long)r.NT * kCostKey + kCostItem);
     const int kvh = (int)quotient(at, head);
     at -= head * kvh;
     const int blk = (int)min(quotient(at, row_cost), (long long)rb);
     at -= row_cost * blk;
-    const int tile = (int)quotient(at, blk < rb ? kCostRow : kCostKey);
+    const int tile = at <= kCostItem ? 0 : (int)quotient(at - kCostItem, blk < rb ? kCostRow : kCostKey);
     if (tile <= kSnap) return make_int4(b, kvh, blk, 0);
     if (r.NT - tile <= kSnap) return next_item(b, kvh, blk, nb, p.Hkv);
     return make_int4(b, kvh, blk, tile);
@@ -591,10 +595,17 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const uint64_t va = sw128_mnmajor_desc(ring + (uint32_t)(slot * SLOT), (uint32_t)kTBlk, 1024u);
                 const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
                 const uint32_t later = u >= 2 ? 1u : 0u;
+                const int steps = (min(kTKeys, s.L + s.T - (s.t0 + i) * kTKeys) + 15) / 16;
                 if (elect_one()) {
+                    if (steps == kTKeys / 16) {
 #pragma unroll
-                    for (int kk = 0; kk < kTKeys / 16; ++kk)            // 16 keys each
-                        umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                        for (int kk = 0; kk < kTKeys / 16; ++kk)        // 16 keys each
+                            umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                    } else {
+#pragma unroll 1
+                        for (int kk = 0; kk < steps; ++kk)
+                            umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                    }
                     if (!s.row_mode || st) umma_commit(empty + 8u * slot);
                     if (u >= s.units - 2) umma_commit(ofin + 8u * st);
                 }
@@ -641,12 +652,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             const int32_t* bt = p.block_tables + (size_t)s.b * p.bt_stride;
             const size_t trow = (size_t)s.row0 + tok0 + rtok;
             const uint32_t* mrow = p.tree_mask + (valid ? trow : (size_t)s.row0) * p.mask_words;
-            // word i of the drafted keys this row sees; all cached keys before them
-            auto seen = [&](int i) -> uint32_t {
-                if (i < 0) return ~0u;
+            // word i of the drafted keys this row sees; all cached keys before
+            // them.  Those of the first 64 are read ahead.
+            auto word = [&](int i) -> uint32_t {
                 if (!valid || 32 * i >= s.T) return 0u;
                 return __ldg(&mrow[i]) & (s.T - 32 * i < 32 ? (1u << (s.T - 32 * i)) - 1u : ~0u);
             };
+            const uint32_t word0 = word(0), word1 = word(1);
+            auto seen = [&](int i) -> uint32_t { return i < 0 ? ~0u : i == 0 ? word0 : i == 1 ? word1 : word(i); };
             // E4M3: lanes 0 .. 7 hold the K scales of a tile's pages, 8 .. 15 the V scales, one tile ahead
             const int step = s.row_mode ? 1 : 2, first = s.row_mode ? 0 : st;
             auto page_of = [&](int i) {
@@ -708,32 +721,34 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     const int z0 = n_keys - key0, d0 = max(0, s.L - key0);
                     if (ok) {
                         bool wrote = false;
-                        for (int x = 32 * quarter + lane; x < (kTKeys - d0) * KB * 8; x += 128) {
-                            const int row = d0 + x / (KB * 8), rem = x % (KB * 8);
-                            const uint32_t addr = va + (uint32_t)((rem >> 3) * kTBlk + row * 128 + (rem & 7) * 16);
-                            if (row >= z0) {
-                                sts128(addr, make_uint4(0u, 0u, 0u, 0u));
-                                wrote = true;
-                                continue;
-                            }
-                            const uint4 v = lds128(addr);
-                            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                            bool odd = false;
+                        const int pieces = (min(kTKeys, (z0 + 15) & ~15) - d0) * KB * 8;      // up to the last step of P V
+                        for (int x0 = 32 * quarter + lane; x0 < pieces; x0 += 512) {
+                            uint4 v[4];
+                            uint32_t addr[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                if ((w[k] & 0x7F80u) == 0x7F80u) {
-                                    w[k] &= 0xFFFF0000u;
-                                    odd = true;
-                                }
-                                if ((w[k] & 0x7F800000u) == 0x7F800000u) {
-                                    w[k] &= 0xFFFFu;
-                                    odd = true;
-                                }
+                                const int x = x0 + 128 * k, row = d0 + x / (KB * 8), rem = x % (KB * 8);
+                                addr[k] = va + (uint32_t)((rem >> 3) * kTBlk + row * 128 + (rem & 7) * 16);
+                                if (x < pieces) v[k] = lds128(addr[k]);
                             }
-                            if (odd) {
-                                sts128(addr, make_uint4(w[0], w[1], w[2], w[3]));
-                                s_odd = 1;
-                                wrote = true;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int x = x0 + 128 * k, row = d0 + x / (KB * 8);
+                                if (x >= pieces) break;
+                                uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+                                bool change = row >= z0;
+#pragma unroll
+                                for (int i2 = 0; i2 < 4; ++i2) {
+                                    const bool lo = (w[i2] & 0x7F80u) == 0x7F80u, hi = (w[i2] & 0x7F800000u) == 0x7F800000u;
+                                    if (row >= z0) w[i2] = 0u;
+                                    else if (lo || hi) {
+                                        w[i2] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
+                                        change = true;
+                                        s_odd = 1;
+                                    }
+                                }
+                                if (change) sts128(addr[k], make_uint4(w[0], w[1], w[2], w[3]));
+                                wrote = wrote || change;
                             }
                         }
                         if (wrote) fence_proxy_async_smem();
