@@ -27,10 +27,10 @@
 // unnormalised O, m and l go to the workspace and are merged by tree_combine
 // in a fixed order.  Nothing waits for another CTA.
 //
-// Warps: 0 loads Q and K (TMA), the last one V, 1 issues the MMAs, 2 .. 9
-// softmax and output, one thread per row; for E4M3 pools 10 .. 13 turn the codes into bf16 tiles
-// (exact; the scales of a page and head go into the scores and the weights in
-// fp32).  P is rounded to bf16 for the matrix product, each weight off by at
+// Warps: 0 loads Q and K (TMA), 2 loads V, 1 issues the MMAs, 4 .. 11 softmax
+// and output, one thread per row; for E4M3 pools 12 .. 19 turn the codes into
+// bf16 tiles (exact; the scales of a page and head go into the scores and the
+// weights in fp32).  P is rounded to bf16 for the matrix product, each weight off by at
 // most 2^-8 of itself; two terms of bf16 would cost half as much again on the
 // tensor pipe, which bounds the large trees.
 #include "tree_params.h"
@@ -55,6 +55,10 @@ constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // 14.2 thousand an item.  Cut by tiles alone, the slowest CTA took 1.5 to 2
 // times the mean.
 constexpr int kCostRow = 4, kCostKey = 2, kCostItem = 9;
+#ifndef PKV_TREE_POLY
+#define PKV_TREE_POLY 2
+#endif
+constexpr int kPoly = PKV_TREE_POLY;          // of every 8 pairs of weights, those whose 2^x goes to the FMA pipe
 constexpr int kSnap = 2;                      // a cut this near to an item's ends moves there
 
 template <int D, bool FP8>
@@ -64,7 +68,7 @@ struct TreeGeo {
     static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
     static constexpr int NC = FP8 ? (D == 128 ? 4 : 6) : 0;          // tiles of codes
     static constexpr int STG = kTKeys * D;
-    static constexpr int THREADS = 64 + 256 + (FP8 ? 128 : 0) + 32;
+    static constexpr int THREADS = 128 + 256 + (FP8 ? 256 : 0);
     static constexpr int BYTES = (2 + NS) * SLOT + NC * STG + 1024;
 };
 
@@ -87,12 +91,12 @@ struct Request {
 // (its rows are zero).
 __device__ __forceinline__ int read_request(const TreeAttnParams& p, int b, Request& r)
 {
-    const int a = p.cu_q[b], e = p.cu_q[b + 1];
+    const int a = __ldg(&p.cu_q[b]), e = __ldg(&p.cu_q[b + 1]);
+    r.L = __ldg(&p.seq_lens[b]);
     if (a < 0 || e > p.n_tokens || a > e) return 2;
     r.row0 = a;
     r.T = e - a;
     if (r.T == 0) return 0;
-    r.L = p.seq_lens[b];
     const long long keys = (long long)r.L + r.T;
     if (r.L < 0 || keys > (long long)p.bt_stride * p.P || r.T > 32ll * p.mask_words) return 3;
     r.NT = (int)((keys + kTKeys - 1) / kTKeys);
@@ -212,6 +216,65 @@ __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 
 // ---- softmax of one tile --------------------------------------------------------
 
+// Pairs of fp32 in one 64-bit register, and their arithmetic.
+__device__ __forceinline__ uint64_t two(float a, float b)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float first_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float second_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b)
+{
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// 2^z of a pair on the FMA pipe, z at most 8: the whole number n nearest z by
+// adding and taking away 1.5 2^23 (its low bits are then those of the sum), 2^(z
+// - n) by a polynomial of degree 3 (minimax in the relative error on [-1/2,
+// 1/2], found by Remez exchange: 7.5e-5, far below the 2^-8 of the bf16 that the
+// weight becomes), n added to the exponent.  Below 2^-126 it stays there: a row
+// that sees nothing is told by its reference, -inf, not by its sum.
+__device__ __forceinline__ uint64_t exp2_poly(uint64_t z)
+{
+    constexpr float kShift = 12582912.f;
+    z = two(max_nan(first_of(z), -126.f), max_nan(second_of(z), -126.f));
+    const uint64_t t = add2(z, two(kShift, kShift));
+    const uint64_t x = fma2(add2(t, two(-kShift, -kShift)), two(-1.f, -1.f), z);
+    uint64_t y = fma2(x, two(0.05517166852951f, 0.05517166852951f), two(0.24261112511158f, 0.24261112511158f));
+    y = fma2(x, y, two(0.69326096773148f, 0.69326096773148f));
+    y = fma2(x, y, two(0.99992805719376f, 0.99992805719376f));
+    return two(__uint_as_float((uint32_t)y + ((uint32_t)t << 23)),
+               __uint_as_float((uint32_t)(y >> 32) + ((uint32_t)(t >> 32) << 23)));
+}
+
 // The scores of keys that the row does not see become -inf, whatever they
 // were (of tiles with drafted keys, or pages out of range, before the pass
 // below: masks in that pass would double its code for one tile in many).
@@ -281,17 +344,16 @@ __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool 
             }
         }
         tmem_wait_ld();
-        float g[N / 16][4];                                    // short chains: one warp alone has to fill its pipes
-#pragma unroll
-        for (int c = 0; c < N; ++c) {
-            const float v = __uint_as_float(x[c]);
-            float& y = g[c >> 4][c & 3];
-            y = (c & 15) < 4 ? v : fmaxf(y, v);
-        }
         float mx = -INFINITY;
 #pragma unroll
-        for (int h = 0; h < N / 16; ++h) {
-            const float y = fmaxf(fmaxf(g[h][0], g[h][1]), fmaxf(g[h][2], g[h][3]));
+        for (int h = 0; h < N / 16; ++h) {                     // short chains: one warp alone has to fill its pipes
+            float g[4];
+#pragma unroll
+            for (int k2 = 0; k2 < 4; ++k2) {
+                const float* y = reinterpret_cast<const float*>(&x[16 * h + 4 * k2]);
+                g[k2] = fmaxf(max3(y[0], y[1], y[2]), y[3]);
+            }
+            const float y = fmaxf(max3(g[0], g[1], g[2]), g[3]);
             mx = fmaxf(mx, FP8 ? y * fs[h] : y);
         }
         if (!FP8) mx *= f;
@@ -308,30 +370,25 @@ __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool 
             m = mn;
         }
         const float mref = m == -INFINITY ? 0.f : m;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint64_t m2 = two(-mref, -mref);
+        uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int h = 0; h < N / 16; ++h) {                     // 16 keys: 8 columns
+            const uint64_t f2 = FP8 ? two(fs[h], fs[h]) : two(f, f);
             uint32_t w[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = 16 * h + 2 * i;
-                float p0 = ex2(fmaf(__uint_as_float(x[c]), FP8 ? fs[h] : f, -mref));
-                float p1 = ex2(fmaf(__uint_as_float(x[c + 1]), FP8 ? fs[h] : f, -mref));
-                if (FP8) {          // the V scale goes into the weights that P V takes, not into their sum
-                    sum[2 * (i & 1)] += p0;
-                    sum[2 * (i & 1) + 1] += p1;
-                    p0 *= vs[h];
-                    p1 *= vs[h];
-                    w[i] = pack_bf16(p0, p1);
-                } else {            // the sum of what P V takes: the weights add up to what divides them
-                    w[i] = pack_bf16(p0, p1);
-                    sum[2 * (i & 1)] += bf16_lo(w[i]);
-                    sum[2 * (i & 1) + 1] += bf16_hi(w[i]);
-                }
+                const uint64_t z = fma2(two(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2, m2);
+                uint64_t e = i % 8 < kPoly ? exp2_poly(z) : two(ex2(first_of(z)), ex2(second_of(z)));
+                sum[i & 1] = add2(sum[i & 1], e);
+                if (FP8) e = mul2(e, two(vs[h], vs[h]));       // the V scale goes into what P V takes, not into the sum
+                w[i] = pack_bf16(first_of(e), second_of(e));
             }
             tmem_st8(scol + (uint32_t)(N / 2 * k + 8 * h), w);
         }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        const uint64_t all = add2(sum[0], sum[1]);
+        l += first_of(all) + second_of(all);
     }
     tmem_wait_st();
 }
@@ -395,17 +452,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         fence_mbar_init();
     }
 
+    if (warp == 1) {
+        __syncwarp();
+        tmem_alloc(smem_u32(&s_tmem), kTCols);
+    }
+
     // ---- where this CTA's run starts and ends
     {
         const int per = (p.batch + THREADS - 1) / THREADS;
         const int lo = min(p.batch, tid * per), hi = min(p.batch, lo + per);
         long long mine = 0;
-        int err = 0;
+        int err = 0, zero = 0;
         Request r;
         for (int b = lo; b < hi; ++b) {
             const int st = read_request(p, b, r);
             if (st == 1) mine += cost_of(p, r);
             else if (st) err = kErrLength;
+            zero |= st == 3;
         }
         if (err && cta == 0) atomicOr(p.err, err);
         long long incl = mine;
@@ -416,18 +479,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         }
         if (lane == 31) s_scan[warp] = incl;
         if (tid < 2) s_pos[tid] = make_int4(p.batch, 0, 0, 0);
-        __syncthreads();
+        tmem_fence_before();
+        zero = __syncthreads_or(zero);
+        tmem_fence_after();
         long long pre = incl - mine, total = 0;
+#pragma unroll
         for (int w = 0; w < WARPS; ++w) {
-            if (w < warp) pre += s_scan[w];
-            total += s_scan[w];
+            const long long x = s_scan[w];
+            if (w < warp) pre += x;
+            total += x;
         }
+#pragma unroll
         for (int k = 0; k < 2; ++k) {
             const long long x = quotient(total * (cta + k), W);
             if (x < pre || x >= pre + mine) continue;
             long long at = pre;
             for (int b = lo; b < hi; ++b) {
-                if (read_request(p, b, r) != 1) continue;
+                if (per > 1 && read_request(p, b, r) != 1) continue;      // with one request a thread, r is it
                 const long long c = cost_of(p, r);
                 if (x < at + c) {
                     s_pos[k] = place_at(p, b, r, x - at);
@@ -439,7 +507,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         __syncthreads();
         if (tid < 2 && (tid == 0 || cta == W - 1)) p.pos[cta + tid] = s_pos[tid];
         // rows of requests whose lengths are out of range
-        for (int b = cta; b < p.batch; b += W) {
+        for (int b = cta; zero && b < p.batch; b += W) {
             if (read_request(p, b, r) != 3) continue;
             uint4* dst = reinterpret_cast<uint4*>(p.out + (size_t)r.row0 * p.Hq * D);
             const size_t n = (size_t)r.T * p.Hq * D / 8;
@@ -449,22 +517,24 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
     Walk walk;
     walk.cur = s_pos[0];
     walk.end = s_pos[1];
-    if (!before(walk.cur, walk.end)) return;      // the whole CTA
-
-    if (warp == 1) {
-        __syncwarp();
-        tmem_alloc(smem_u32(&s_tmem), kTCols);
-    }
-    tmem_fence_before();
-    __syncthreads();
-    tmem_fence_after();
     const uint32_t tmem = s_tmem;
+    if (!before(walk.cur, walk.end)) {            // nothing for the whole CTA
+        if (warp == 1) {
+            __syncwarp();
+            tmem_dealloc(tmem, kTCols);
+        }
+        return;
+    }
     Segment s;
 
-    if (warp == 0 || warp == WARPS - 1) {
-        // ---- loads: warp 0 those of Q and K, the last warp those of V (a box
-        // takes about 100 cycles to issue; one warp alone was what bounded
-        // pages of 16 tokens)
+    // E4M3: 640 threads of 96 registers at the start; the softmax takes what the
+    // others do not need (144 x 256 + 64 x 384 = 96 x 640)
+    if (warp < 4) {
+    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (warp == 0 || warp == 2) {
+        // ---- loads: warp 0 those of Q and K, warp 2 those of V (a box takes
+        // about 100 cycles to issue; one warp alone was what bounded pages of
+        // 16 tokens)
         const bool is_v = warp != 0;
         const CUtensorMap* const map = is_v ? &tmv : &tmk;
         constexpr int N = FP8 ? NCX : NS;
@@ -551,51 +621,60 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
         };
         while (ok && walk.next(p, s)) {
-            // what S(u) reads has landed
-            auto score_ready = [&](int u) {
-                const int i = s.row_mode ? u >> 1 : u, seq = rb + k_seq(s, i);
-                if (u == 0 || (u == 1 && s.row_mode)) {
-                    const int qb = s.row_mode ? u : qsel;
-                    wait(qfull + 8u * qb, qb ? qc1 : qc0);
-                    if (qb) ++qc1;
-                    else ++qc0;
-                }
-                wait(full + 8u * (seq % NS), seq / NS);
+            const int qb0 = s.row_mode ? 0 : qsel, qb1 = s.row_mode ? 1 : qsel;
+            auto tile_of = [&](int u) { return s.row_mode ? u >> 1 : u; };
+            auto k_bar = [&](int u, int& phase) {
+                const int seq = rb + k_seq(s, tile_of(u));
+                phase = seq / NS;
+                return seq % NS;
             };
-            auto score = [&](int u) {
-                const int st = u & 1, i = s.row_mode ? u >> 1 : u;
-                const int slot = (rb + k_seq(s, i)) % NS;
-                const int qb = s.row_mode ? st : qsel;
-                if (!ok) return;
-                tmem_fence_after();
+            // the instructions of S(u), by the elected lane
+            auto score = [&](int u, int slot) {
+                const int st = u & 1, qb = st ? qb1 : qb0;
                 const uint64_t qa = sw128_kmajor_desc(q0 + (uint32_t)(qb * SLOT)),
                                ka = sw128_kmajor_desc(ring + (uint32_t)(slot * SLOT));
                 const uint32_t dcol = tmem + (uint32_t)(st * kTKeys);
-                if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kTBlk + (kk & 3) * 32) >> 4);
-                        umma_bf16_all(dcol, qa + off, ka + off, idS, kk ? 1u : 0u);
-                    }
-                    umma_commit(sfull + 8u * st);
-                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
-                    if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) umma_commit(qempty + 8u * qb);
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint64_t off = (uint64_t)(((kk >> 2) * kTBlk + (kk & 3) * 32) >> 4);
+                    umma_bf16_all(dcol, qa + off, ka + off, idS, kk ? 1u : 0u);
                 }
-                __syncwarp();
+                umma_commit(sfull + 8u * st);
+                if (!s.row_mode || st) umma_commit(empty + 8u * slot);
+                if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) umma_commit(qempty + 8u * qb);
             };
-            auto values = [&](int u) {
-                const int st = u & 1, i = s.row_mode ? u >> 1 : u;
-                const int seq = rb + v_seq(s, i), slot = seq % NS;
-                wait(full + 8u * slot, seq / NS);
+            wait(qfull + 8u * qb0, qb0 ? qc1 : qc0);
+            if (s.row_mode) wait(qfull + 8u, qc1);
+            if (s.row_mode || qb0) ++qc1;
+            if (s.row_mode || !qb0) ++qc0;
+            for (int u = 0; u < 2 && u < s.units; ++u) {
+                int phase;
+                const int slot = k_bar(u, phase);
+                wait(full + 8u * slot, phase);
+                if (!ok) break;
+                tmem_fence_after();
+                if (elect_one()) score(u, slot);
+                __syncwarp();
+            }
+            // P V(u) and S(u + 2) go out together once P(u) is written; that K
+            // has landed is looked at while P is awaited
+            for (int u = 0; ok && u < s.units; ++u) {
+                const int st = u & 1, i = tile_of(u);
+                const int vseq = rb + v_seq(s, i), vslot = vseq % NS;
+                const bool next = u + 2 < s.units;
+                int kphase = 0, kslot = 0;
+                if (next) kslot = k_bar(u + 2, kphase);
+                wait(full + 8u * vslot, vseq / NS);
+                const bool k_here = next && __all_sync(0xffffffffu, mbar_try_wait(full + 8u * kslot, (uint32_t)(kphase & 1)));
+                const int steps = (min(kTKeys, s.L + s.T - (s.t0 + i) * kTKeys) + 15) / 16;
+                const uint64_t va = sw128_mnmajor_desc(ring + (uint32_t)(vslot * SLOT), (uint32_t)kTBlk, 1024u);
+                const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
+                const uint32_t later = u >= 2 ? 1u : 0u;
                 wait(pfull + 8u * st, st ? pc1 : pc0);
                 if (st) ++pc1;
                 else ++pc0;
-                if (!ok) return;
+                if (!ok) break;
                 tmem_fence_after();
-                const uint64_t va = sw128_mnmajor_desc(ring + (uint32_t)(slot * SLOT), (uint32_t)kTBlk, 1024u);
-                const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
-                const uint32_t later = u >= 2 ? 1u : 0u;
-                const int steps = (min(kTKeys, s.L + s.T - (s.t0 + i) * kTKeys) + 15) / 16;
                 if (elect_one()) {
                     if (steps == kTKeys / 16) {
 #pragma unroll
@@ -606,22 +685,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                         for (int kk = 0; kk < steps; ++kk)
                             umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
                     }
-                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
-                    if (u >= s.units - 2) umma_commit(ofin + 8u * st);
+                    if (!s.row_mode || st) umma_commit(empty + 8u * vslot);
+                    if (!next) umma_commit(ofin + 8u * st);
+                    if (k_here) score(u + 2, kslot);
                 }
                 __syncwarp();
-            };
-            score_ready(0);
-            score(0);
-            if (s.units > 1) {
-                score_ready(1);
-                score(1);
-            }
-            for (int u = 0; ok && u < s.units; ++u) {
-                values(u);
-                if (u + 2 < s.units) {
-                    score_ready(u + 2);
-                    score(u + 2);
+                if (next && !k_here) {
+                    wait(full + 8u * kslot, kphase);
+                    if (!ok) break;
+                    if (elect_one()) score(u + 2, kslot);
+                    __syncwarp();
                 }
             }
             if (!s.row_mode) qsel ^= 1;
@@ -631,9 +704,11 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         if (elect_one()) umma_commit(drain);                   // every MMA has ended before the tensor memory is given back
         (void)mbar_wait_bounded(drain, 0u, kTWaitNs);
         __syncwarp();
-    } else if (warp < 10) {
+    }
+    } else if (warp < 12) {
+        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         // ---- softmax and output: row r of stream st
-        const int st = (warp - 2) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
+        const int st = (warp - 4) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const int rtok = r / p.G, g = r - rtok * p.G;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t scol = lanes + (uint32_t)(st * kTKeys);
@@ -789,7 +864,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             if (ok && act) {
                 const bool both = !s.row_mode && s.n > 1;
                 const int cols = s.row_mode ? D : D / 2, col0 = s.row_mode ? 0 : st * (D / 2);
-                const float inv = l == 0.f ? 0.f : 1.f / l;
+                const float inv = m == -INFINITY ? 0.f : 1.f / l;      // -inf: the row sees nothing
                 const bool odd = *(volatile int*)&s_odd != 0;
                 const size_t slot_row = ((size_t)(2 * cta + (s.place == 1)) * 2 * kTRows) + (s.row_mode ? st * kTRows : 0) + r;
                 __nv_bfloat16* const orow = p.out + (trow * p.Hq + (size_t)s.kvh * p.G + g) * D;
@@ -848,29 +923,35 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             rb += 2 * s.n;
         }
         if (!ok) s_fail = 1;
-    } else if (FP8) {       // warps 10 .. 13
-        // ---- codes to bf16: lane l of a warp takes row 8 k + l % 8, 16 codes l / 8 + 4 j
-        const int w = warp - 10;
-        int q = 0;
+    } else if (FP8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        // ---- codes to bf16: warps 12 .. 15 the even loads, 16 .. 19 the odd
+        // ones; lane l of a warp takes row 8 k + l % 8, 16 codes l / 8 + 4 j
+        const int w = warp & 3;
+        int rb = 0;
         bool ok = true;
         while (ok && walk.next(p, s)) {
-            for (int e = q + 2 * s.n; ok && q < e; ++q) {
+            const int end = rb + 2 * s.n;
+            for (int q = rb + ((rb ^ ((warp - 12) >> 2)) & 1); q < end; q += 2) {
                 const int c = q % NCX, slot = q % NS;
                 ok = __all_sync(0xffffffffu, wait_bar(cfull + 8u * c, (uint32_t)((q / NCX) & 1))) != 0;
-                if (ok && q >= NS)
-                    ok = __all_sync(0xffffffffu, wait_bar(empty + 8u * slot, (uint32_t)((q / NS - 1) & 1))) != 0;
+                if (ok && q >= NS) ok = __all_sync(0xffffffffu, wait_bar(empty + 8u * slot, (uint32_t)((q / NS - 1) & 1))) != 0;
                 if (!ok) break;
                 const uint32_t src = stage + (uint32_t)(c * Gm::STG), dst = ring + (uint32_t)(slot * SLOT);
+#pragma unroll 1
+                for (int j = 0; j < D / 64; ++j) {
+                    const int ch = (lane >> 3) + 4 * j;                  // 16 codes: d 16 ch ..
+                    uint4 v[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int row = 32 * w + 8 * k + (lane & 7);
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = 32 * w + 8 * k + (lane & 7);
+                        v[k] = lds128(src + (D == 128 ? (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4))
+                                                      : (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4))));
+                    }
 #pragma unroll
-                    for (int j = 0; j < D / 64; ++j) {
-                        const int ch = (lane >> 3) + 4 * j;                  // 16 codes: d 16 ch ..
-                        const uint32_t at = D == 128 ? (uint32_t)(row * 128 + ((ch ^ (row & 7)) << 4))
-                                                     : (uint32_t)(row * 64 + ((ch ^ ((row >> 1) & 3)) << 4));
-                        const uint4 v = lds128(src + at);
-                        const uint32_t in[4] = {v.x, v.y, v.z, v.w};
+                    for (int k = 0; k < 4; ++k) {
+                        const int row = 32 * w + 8 * k + (lane & 7);
+                        const uint32_t in[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
                         uint32_t o[8];
 #pragma unroll
                         for (int x = 0; x < 4; ++x) {
@@ -891,6 +972,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     mbar_arrive(cempty + 8u * c);
                 }
             }
+            rb = end;
         }
         if (!ok) s_fail = 1;
     }
@@ -976,7 +1058,7 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
         }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
+        const float inv = m == -INFINITY ? 0.f : 1.f / l;
         __nv_bfloat16* dst = p.out + (((size_t)r.row0 + first + tok) * p.Hq + (size_t)x.y * p.G + g) * D + lane * E;
         if (E == 4)
             *reinterpret_cast<uint2*>(dst) =
