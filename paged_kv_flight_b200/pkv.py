@@ -501,6 +501,42 @@ def _rows(x, shape, name):
                          f"got {tuple(x.shape)}")
 
 
+_Tensor, _i32, _bf16 = torch.Tensor, torch.int32, torch.bfloat16
+
+
+def _vec(x, n, name):
+    """Device pointer of an int32 vector of n entries (_rows, then _ptr; the
+    calls of a small step are bound by the host, so what is right takes one
+    line)."""
+    if type(x) is _Tensor and x.dtype is _i32 and x.is_cuda and x.dim() == 1 and x.numel() == n and x.is_contiguous():
+        return x.data_ptr()
+    _rows(x, (n,), name)
+    return _ptr(x, _I32, name)
+
+
+def _mat(x, shape, name):
+    """The same of an int32 tensor of the given shape."""
+    if type(x) is _Tensor and x.dtype is _i32 and x.is_cuda and x.shape == shape and x.is_contiguous():
+        return x.data_ptr()
+    _rows(x, shape, name)
+    return _ptr(x, _I32, name)
+
+
+def _act(x, shape, name):
+    """The same of a bf16 tensor of the given shape."""
+    if type(x) is _Tensor and x.dtype is _bf16 and x.is_cuda and x.shape == shape and x.is_contiguous():
+        return x.data_ptr()
+    _rows(x, shape, name)
+    return _ptr(x, _ACT, name)
+
+
+def _sizes(x, n, name):
+    """The sizes of a tensor of n dimensions."""
+    if not isinstance(x, _Tensor) or x.dim() != n:
+        raise ValueError(f"{name}: expected a tensor of {n} dimensions")
+    return x.shape
+
+
 def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, free_count, cu_q, slots, positions,
                  pages_out, free_left, parents=None, tree_mask=None, stream=None, check: bool = True) -> int:
     """Pages for every request's new tokens (off the stack free_pages[:
@@ -508,23 +544,17 @@ def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, 
     and positions [capacity] (-1 behind the last token); with parents
     [capacity] also the ancestor masks tree_mask [capacity, words].  pages_out
     [batch] may be pages_held and free_left [1] may be free_count (in place)."""
-    batch, stride = int(block_tables.shape[0]), int(block_tables.shape[1])
-    n_tokens = int(slots.shape[0])
-    for x, shape, name in ((seq_lens, (batch,), "seq_lens"), (new_lens, (batch,), "new_lens"),
-                           (pages_held, (batch,), "pages_held"), (pages_out, (batch,), "pages_out"),
-                           (cu_q, (batch + 1,), "cu_q"), (positions, (n_tokens,), "positions"),
-                           (free_pages, (None,), "free_pages"), (free_count, (1,), "free_count"),
-                           (free_left, (1,), "free_left"), (parents, (n_tokens,), "parents"),
-                           (tree_mask, (n_tokens, None), "tree_mask")):
-        _rows(x, shape, name)
-    st = lib.pkv_slot_map(ctx, _ptr(seq_lens, _I32, "seq_lens"), _ptr(new_lens, _I32, "new_lens"),
-                          _ptr(parents, _I32, "parents"), batch, _ptr(block_tables, _I32, "block_tables"), stride,
-                          _ptr(pages_held, _I32, "pages_held"), _ptr(pages_out, _I32, "pages_out"),
-                          _ptr(free_pages, _I32, "free_pages"), int(free_pages.shape[0]),
-                          _ptr(free_count, _I32, "free_count"), _ptr(free_left, _I32, "free_left"), n_tokens,
-                          0 if tree_mask is None else int(tree_mask.shape[1]), _ptr(cu_q, _I32, "cu_q"),
-                          _ptr(slots, _I32, "slots"), _ptr(positions, _I32, "positions"),
-                          _ptr(tree_mask, _I32, "tree_mask"), _stream(stream))
+    B, stride = _sizes(block_tables, 2, "block_tables")
+    n, = _sizes(slots, 1, "slots")
+    cap, = _sizes(free_pages, 1, "free_pages")
+    words = 0 if tree_mask is None else _sizes(tree_mask, 2, "tree_mask")[1]
+    st = lib.pkv_slot_map(ctx, _vec(seq_lens, B, "seq_lens"), _vec(new_lens, B, "new_lens"),
+                          None if parents is None else _vec(parents, n, "parents"), B,
+                          _mat(block_tables, (B, stride), "block_tables"), stride, _vec(pages_held, B, "pages_held"),
+                          _vec(pages_out, B, "pages_out"), _vec(free_pages, cap, "free_pages"), cap,
+                          _vec(free_count, 1, "free_count"), _vec(free_left, 1, "free_left"), n, words,
+                          _vec(cu_q, B + 1, "cu_q"), _vec(slots, n, "slots"), _vec(positions, n, "positions"),
+                          None if tree_mask is None else _mat(tree_mask, (n, words), "tree_mask"), _stream(stream))
     return _done(st, "pkv_slot_map", check)
 
 
@@ -533,17 +563,16 @@ def pkv_rope_append_axes(ctx, q, k_new, v_new, positions, sections, slots, q_out
     """q / q_out [n_tokens, Hq, d] (q_out may be q), k_new / v_new [n_tokens,
     Hkv, d], positions [axes, n_tokens], slots [n_tokens] (page * page_size +
     place, -1 skips the token); sections: pairs of each axis, d / 2 in all."""
-    n, d = int(q.shape[0]), int(q.shape[2])
-    _rows(k_new, (n, None, d), "k_new")
-    _rows(v_new, tuple(k_new.shape), "v_new")
-    _rows(positions, (len(sections), n), "positions")
-    _rows(slots, (n,), "slots")
-    _rows(q_out, tuple(q.shape), "q_out")
-    sec = (_I * len(sections))(*(int(x) for x in sections))
-    st = lib.pkv_rope_append_axes(ctx, _ptr(q, _ACT, "q"), _ptr(k_new, _ACT, "k_new"), _ptr(v_new, _ACT, "v_new"), n,
-                                  _ptr(positions, _I32, "positions"), len(sections), sec, int(bool(interleaved)),
-                                  _ptr(slots, _I32, "slots"), _ptr(q_out, _ACT, "q_out"),
-                                  *_kv(k_pool, v_pool, k_scale, v_scale), _stream(stream))
+    q_shape = _sizes(q, 3, "q")
+    k_shape = _sizes(k_new, 3, "k_new")
+    n, axes = q_shape[0], len(sections)
+    if k_shape[0] != n or k_shape[2] != q_shape[2]:
+        raise ValueError(f"k_new: shape {tuple(k_shape)} next to q of {tuple(q_shape)}")
+    st = lib.pkv_rope_append_axes(ctx, _act(q, q_shape, "q"), _act(k_new, k_shape, "k_new"),
+                                  _act(v_new, k_shape, "v_new"), n, _mat(positions, (axes, n), "positions"), axes,
+                                  (_I * axes)(*sections), 1 if interleaved else 0, _vec(slots, n, "slots"),
+                                  _act(q_out, q_shape, "q_out"), *_kv(k_pool, v_pool, k_scale, v_scale),
+                                  _stream(stream))
     return _done(st, "pkv_rope_append_axes", check)
 
 
@@ -552,16 +581,15 @@ def pkv_decode_attn_tree(ctx, q, k_pool, v_pool, k_scale, v_scale, block_tables,
     """q / out [n_tokens, Hq, d]; cu_q [batch + 1] int32; tree_mask [n_tokens,
     words] int32: bit j % 32 of word j / 32 lets the row see new token j of
     its request (the cached tokens are always seen)."""
-    batch, n = int(seq_lens.shape[0]), int(q.shape[0])
-    _rows(block_tables, (batch, None), "block_tables")
-    _rows(cu_q, (batch + 1,), "cu_q")
-    _rows(tree_mask, (n, None), "tree_mask")
-    _rows(out, tuple(q.shape), "out")
-    st = lib.pkv_decode_attn_tree(ctx, _ptr(q, _ACT, "q"), *_kv(k_pool, v_pool, k_scale, v_scale),
-                                  _ptr(block_tables, _I32, "block_tables"), int(block_tables.shape[1]),
-                                  _ptr(seq_lens, _I32, "seq_lens"), _ptr(cu_q, _I32, "cu_q"),
-                                  _ptr(tree_mask, _I32, "tree_mask"), int(tree_mask.shape[1]), batch, n,
-                                  _ptr(out, _ACT, "out"), _stream(stream))
+    q_shape = _sizes(q, 3, "q")
+    B, stride = _sizes(block_tables, 2, "block_tables")
+    words = _sizes(tree_mask, 2, "tree_mask")[1]
+    n = q_shape[0]
+    st = lib.pkv_decode_attn_tree(ctx, _act(q, q_shape, "q"), *_kv(k_pool, v_pool, k_scale, v_scale),
+                                  _mat(block_tables, (B, stride), "block_tables"), stride,
+                                  _vec(seq_lens, B, "seq_lens"), _vec(cu_q, B + 1, "cu_q"),
+                                  _mat(tree_mask, (n, words), "tree_mask"), words, B, n, _act(out, q_shape, "out"),
+                                  _stream(stream))
     return _done(st, "pkv_decode_attn_tree", check)
 
 
@@ -569,13 +597,10 @@ def pkv_tree_commit(ctx, k_pool, v_pool, k_scale, v_scale, block_tables, seq_len
                     stream=None, check: bool = True) -> int:
     """path [batch, depth] int32, its first path_lens[b] entries the accepted
     new tokens of request b in rising order; lens_out [batch] may be seq_lens."""
-    batch = int(seq_lens.shape[0])
-    _rows(block_tables, (batch, None), "block_tables")
-    _rows(path, (batch, None), "path")
-    _rows(path_lens, (batch,), "path_lens")
-    _rows(lens_out, (batch,), "lens_out")
-    st = lib.pkv_tree_commit(ctx, *_kv(k_pool, v_pool, k_scale, v_scale), _ptr(block_tables, _I32, "block_tables"),
-                             int(block_tables.shape[1]), _ptr(seq_lens, _I32, "seq_lens"), _ptr(path, _I32, "path"),
-                             int(path.shape[1]), _ptr(path_lens, _I32, "path_lens"), batch,
-                             _ptr(lens_out, _I32, "lens_out"), _stream(stream))
+    B, stride = _sizes(block_tables, 2, "block_tables")
+    depth = _sizes(path, 2, "path")[1]
+    st = lib.pkv_tree_commit(ctx, *_kv(k_pool, v_pool, k_scale, v_scale),
+                             _mat(block_tables, (B, stride), "block_tables"), stride, _vec(seq_lens, B, "seq_lens"),
+                             _mat(path, (B, depth), "path"), depth, _vec(path_lens, B, "path_lens"), B,
+                             _vec(lens_out, B, "lens_out"), _stream(stream))
     return _done(st, "pkv_tree_commit", check)

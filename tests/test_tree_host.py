@@ -136,9 +136,15 @@ def test_tree_commit_refusals(pkv, fp8):
 
 
 def test_binding_checks_shapes(pkv):
-    """The Python binding holds the tensors' shapes against one another."""
-    i = lambda *s: torch.zeros(*s, dtype=torch.int32)   # noqa: E731
-    h = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)   # noqa: E731
+    """The Python binding holds the tensors' shapes against one another (host
+    tensors that report themselves as device tensors)."""
+    class _OnDevice(torch.Tensor):
+        @property
+        def is_cuda(self):
+            return True
+
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32).as_subclass(_OnDevice)   # noqa: E731
+    h = lambda *s: torch.zeros(*s, dtype=torch.bfloat16).as_subclass(_OnDevice)   # noqa: E731
     ctx = _ctx(pkv)
     with pytest.raises(ValueError, match="cu_q"):
         pkv.pkv_slot_map(ctx, i(4), i(4), i(4, 8), i(4), i(20), i(1), i(4), i(9), i(9), i(4), i(1))
@@ -151,6 +157,13 @@ def test_binding_checks_shapes(pkv):
         pkv.pkv_decode_attn_tree(ctx, h(9, 32, 128), 0, 0, None, None, i(2, 4), i(2), i(3), i(8, 1), h(9, 32, 128))
     with pytest.raises(ValueError, match="path_lens"):
         pkv.pkv_tree_commit(ctx, 0, 0, None, None, i(2, 4), i(2), i(2, 3), i(3), i(2))
+    with pytest.raises(ValueError, match="k_new"):
+        pkv.pkv_rope_append_axes(ctx, h(9, 32, 128), h(8, 8, 128), h(8, 8, 128), i(3, 9), [16, 24, 24], i(9),
+                                 h(9, 32, 128), 0, 0, None, None)
+    with pytest.raises(ValueError, match="device tensors"):
+        pkv.pkv_tree_commit(ctx, 0, 0, None, None, i(2, 4), torch.zeros(2, dtype=torch.int32), i(2, 3), i(2), i(2))
+    with pytest.raises(TypeError, match="path_lens"):
+        pkv.pkv_tree_commit(ctx, 0, 0, None, None, i(2, 4), i(2), i(2, 3), i(2).long(), i(2))
 
 
 def test_plain_forms_agree():
