@@ -201,7 +201,7 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
         return PKV_ERR_CUDA;
     }
 
-    // [error word, chunk counter, slot-map counter | split geometry | partial rows | partial (m, l)];
+    // [error word, chunk counter | split geometry | partial rows | partial (m, l)];
     // two partial slots per unit of the split: G rows each for one new token
     // per request (up to kMaxTailChunks + 1 units per warp), up to
     // kMaxTokenRows rows for several (one unit per warp)
@@ -227,7 +227,6 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
     uint8_t* base = static_cast<uint8_t*>(ctx->ws);
     ctx->d_err = reinterpret_cast<int*>(base);
     ctx->d_claim = reinterpret_cast<int*>(base + 128);
-    ctx->d_done = reinterpret_cast<unsigned*>(base + 192);
     ctx->tail_chunks = pkv::kDefaultTailChunks;
     ctx->d_meta = reinterpret_cast<int*>(base + b_err);
     ctx->d_part_o = reinterpret_cast<float*>(base + b_err + b_cnt);

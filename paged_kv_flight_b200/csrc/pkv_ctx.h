@@ -18,7 +18,6 @@ struct pkv_ctx {
     size_t ws_bytes;
     int* d_err;
     int* d_claim;         // chunk counter of the attention's dynamic tail
-    unsigned* d_done;     // CTAs of a slot-map launch that have finished reading
     double* d_theta;      // [head_dim / 2] rope_base^(-2i/d), fp64
     int* d_meta;
     int vmax;             // virtual requests a varlen attention call may have (bf16 pools)

@@ -27,6 +27,8 @@ pkv_status check_device(const pkv_ctx* ctx)
     return dev == ctx->device ? PKV_OK : PKV_ERR_INVALID_ARG;
 }
 
+int page_shift(int page_size) { return page_size == 16 ? 4 : page_size == 32 ? 5 : 6; }
+
 pkv_status launched(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
 }  // namespace
@@ -83,7 +85,6 @@ pkv_status pkv_slot_map(pkv_ctx* ctx, const int32_t* seq_lens, const int32_t* ne
     p.slots = slots;
     p.positions = positions;
     p.tree_mask = tree_mask;
-    p.done = ctx->d_done;
     p.err = ctx->d_err;
     p.batch = batch;
     p.bt_stride = bt_stride;
@@ -91,6 +92,7 @@ pkv_status pkv_slot_map(pkv_ctx* ctx, const int32_t* seq_lens, const int32_t* ne
     p.n_tokens = n_tokens;
     p.mask_words = mask_words;
     p.P = ctx->cfg.page_size;
+    p.page_shift = page_shift(p.P);
     p.num_pages = ctx->cfg.num_pages;
     return launched(pkv::launch_slot_map(p, stream));
 }
@@ -238,6 +240,7 @@ pkv_status pkv_tree_commit(pkv_ctx* ctx, void* k_pool, void* v_pool, const float
     p.path_stride = path_stride;
     p.Hkv = ctx->cfg.num_kv_heads;
     p.P = ctx->cfg.page_size;
+    p.page_shift = page_shift(p.P);
     p.num_pages = ctx->cfg.num_pages;
     return launched(pkv::launch_tree_commit(p, ctx->cfg.head_dim, ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3, stream));
 }

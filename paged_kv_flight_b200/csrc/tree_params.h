@@ -21,9 +21,8 @@ struct SlotMapParams {
     int32_t* slots;
     int32_t* positions;
     uint32_t* tree_mask;
-    unsigned* done;               // CTAs that have finished reading; wraps to 0 at the end of a launch
     int* err;
-    int batch, bt_stride, free_cap, n_tokens, mask_words, P, num_pages;
+    int batch, bt_stride, free_cap, n_tokens, mask_words, P, page_shift, num_pages;   // P = 1 << page_shift
 };
 cudaError_t slot_map_prepare();
 cudaError_t launch_slot_map(const SlotMapParams& p, cudaStream_t stream);
@@ -87,7 +86,7 @@ struct TreeCommitParams {
     const int32_t* path_lens;
     int32_t* lens_out;            // may be seq_lens
     int* err;
-    int batch, bt_stride, path_stride, Hkv, P, num_pages;
+    int batch, bt_stride, path_stride, Hkv, P, page_shift, num_pages;
 };
 cudaError_t launch_tree_commit(const TreeCommitParams& p, int head_dim, bool fp8, cudaStream_t stream);
 
