@@ -168,6 +168,7 @@ pkv_status pkv_decode_attn_tree(pkv_ctx* ctx, const void* q, const void* k_pool,
     if (overlap(q, bytes, out, bytes)) return PKV_ERR_INVALID_ARG;
     const pkv_status dev = check_device(ctx);
     if (dev != PKV_OK) return dev;
+    if (n_tokens >= 1 << 29) return PKV_ERR_UNSUPPORTED;      // the kernel's reciprocals
 
     const int tb = pkv::kTreeRows / ctx->G;
     if (!pkv::page_maps(ctx, k_pool, v_pool)) return PKV_ERR_CUDA;
@@ -203,6 +204,9 @@ pkv_status pkv_decode_attn_tree(pkv_ctx* ctx, const void* q, const void* k_pool,
     p.part_ml = ctx->d_tree_ml;
     p.pos = ctx->d_tree_pos;
     p.tb = tb;
+    p.g_inv = 65536 / ctx->G + 1;
+    p.two_inv = ((1ull << 37) + 2 * tb - 1) / (2 * tb);
+    p.run_inv = ~0ull / (unsigned)ctx->tree_runs;
     return launched(pkv::launch_tree_attn(p, ctx->tq, ctx->tpk, ctx->tpv, ctx->cfg.head_dim,
                                           ctx->cfg.kv_dtype == PKV_KV_FP8_E4M3, ctx->tree_runs, stream));
 }

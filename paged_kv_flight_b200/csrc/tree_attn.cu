@@ -54,7 +54,8 @@ constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // workloads: 4758 cycles a tile in row mode, 2450 to 2790 in key mode, 10.6 to
 // 14.2 thousand an item.  Cut by tiles alone, the slowest CTA took 1.5 to 2
 // times the mean.
-constexpr int kCostRow = 4, kCostKey = 2, kCostItem = 9;
+constexpr int kCostRowShift = 2, kCostKeyShift = 1, kCostItem = 9;
+constexpr int kCostRow = 1 << kCostRowShift, kCostKey = 1 << kCostKeyShift;
 #ifndef PKV_TREE_POLY
 #define PKV_TREE_POLY 2
 #endif
@@ -107,9 +108,9 @@ __device__ __forceinline__ int read_request(const TreeAttnParams& p, int b, Requ
 // most one in key mode.
 __device__ __forceinline__ void blocks_of(const TreeAttnParams& p, int T, int& row_blocks, int& blocks)
 {
-    const int two = 2 * p.tb;
-    row_blocks = T / two + (T % two > p.tb ? 1 : 0);
-    blocks = (T + two - 1) / two;
+    const int two = 2 * p.tb, whole = (int)(((unsigned long long)T * p.two_inv) >> 37), rest = T - whole * two;
+    row_blocks = whole + (rest > p.tb ? 1 : 0);
+    blocks = whole + (rest > 0 ? 1 : 0);
 }
 
 __device__ __forceinline__ long long cost_of(const TreeAttnParams& p, const Request& r)
@@ -126,13 +127,6 @@ __device__ __forceinline__ bool before(const int4& a, const int4& b)
 }
 __device__ __forceinline__ bool same_item(const int4& a, const int4& b) { return a.x == b.x && a.y == b.y && a.z == b.z; }
 
-// a / b of numbers that are not negative: 64-bit division is called only
-// where it is needed.
-__device__ __forceinline__ long long quotient(long long a, long long b)
-{
-    return (a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
-
 __device__ __forceinline__ int4 next_item(int b, int kvh, int blk, int blocks, int Hkv)
 {
     if (++blk < blocks) return make_int4(b, kvh, blk, 0);
@@ -148,11 +142,10 @@ __device__ __forceinline__ int4 place_at(const TreeAttnParams& p, int b, const R
     blocks_of(p, r.T, rb, nb);
     const long long row_cost = (long long)r.NT * kCostRow + kCostItem,
                     head = row_cost * rb + (nb - rb) * ((long long)r.NT * kCostKey + kCostItem);
-    const int kvh = (int)quotient(at, head);
-    at -= head * kvh;
-    const int blk = (int)min(quotient(at, row_cost), (long long)rb);
-    at -= row_cost * blk;
-    const int tile = at <= kCostItem ? 0 : (int)quotient(at - kCostItem, blk < rb ? kCostRow : kCostKey);
+    int kvh = 0, blk = 0;                   // a few steps: cheaper than divisions in 64 bits
+    for (; at >= head; at -= head) ++kvh;
+    for (; blk < rb && at >= row_cost; at -= row_cost) ++blk;
+    const int tile = at <= kCostItem ? 0 : (int)((at - kCostItem) >> (blk < rb ? kCostRowShift : kCostKeyShift));
     if (tile <= kSnap) return make_int4(b, kvh, blk, 0);
     if (r.NT - tile <= kSnap) return next_item(b, kvh, blk, nb, p.Hkv);
     return make_int4(b, kvh, blk, tile);
@@ -491,7 +484,8 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const long long x = quotient(total * (cta + k), W);
+            const int cut = cta + k;             // total * cut / W, all CTAs by the same arithmetic
+            const long long x = cut == W ? total : (long long)__umul64hi((unsigned long long)total, p.run_inv * (unsigned)cut);
             if (x < pre || x >= pre + mine) continue;
             long long at = pre;
             for (int b = lo; b < hi; ++b) {
@@ -709,7 +703,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         // ---- softmax and output: row r of stream st
         const int st = (warp - 4) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
-        const int rtok = r / p.G, g = r - rtok * p.G;
+        const int rtok = (r * p.g_inv) >> 16, g = r - rtok * p.G;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         const uint32_t scol = lanes + (uint32_t)(st * kTKeys);
         const int shift = 31 - __clz(p.P);
@@ -996,76 +990,71 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
 // ---- merge of the items that the cut went through -----------------------------------
 
 constexpr int kCombineThreads = 256;
-constexpr int kCombineGroups = 16;      // blocks per cut, each a share of the item's rows
+constexpr int kCombineGroups = 4;       // blocks per cut, each a share of the item's rows: one wave of blocks in all
+constexpr int kRowLanes = 16;           // lanes of a row
 
 // Block (i, y): if cut i + 1 is the first inside its item, the parts of that
 // item: the last segment of run i, then the first segments of the runs behind.
+// Bound by a chain of dependent loads (places, lengths, parts): 16 lanes a row
+// keep two rows of 32 bytes a lane in flight in every warp.
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeAttnParams p, int W)
 {
-    constexpr int E = D / 32;
-    __shared__ int s_slot[kMaxTreeRuns];
-    __shared__ float2 s_w[kCombineThreads / 32][kMaxTreeRuns];
-    __shared__ int4 s_pos[kMaxTreeRuns + 1];
+    constexpr int E = D / kRowLanes, ROWS = kCombineThreads / kRowLanes;
+    __shared__ int4 s_pos[kMaxTreeRuns + 2];
+    __shared__ int s_slot[kMaxTreeRuns + 1];
     __shared__ int s_n;
     grid_dependency_wait();
     const int cut = blockIdx.x + 1;
-    const int4 x = p.pos[cut], a = p.pos[cut - 1];
-    if (x.w == 0 || (a.w != 0 && same_item(a, x))) return;
-    Request r;
-    if (read_request(p, x.x, r) != 1) return;
-    const int first = x.z * 2 * p.tb, ntok = min(2 * p.tb, r.T - first), rows = ntok * p.G;
-    if ((int)blockIdx.y * (kCombineThreads / 32) >= rows) return;
-    for (int c = cut + threadIdx.x; c <= W; c += kCombineThreads) s_pos[c] = p.pos[c];
+    for (int c = cut - 1 + threadIdx.x; c <= W; c += kCombineThreads) s_pos[c - (cut - 1)] = p.pos[c];
     __syncthreads();
+    const int4 a = s_pos[0], x = s_pos[1];
+    if (x.w == 0 || (a.w != 0 && same_item(a, x))) return;
     if (threadIdx.x == 0) {
         int n = 0;
         s_slot[n++] = 2 * (cut - 1) + 1;
-        int4 at = x;
-        for (int c = cut; c < W && at.w != 0 && same_item(at, x); ++c) {
-            const int4 to = s_pos[c + 1];
-            if (before(at, to)) s_slot[n++] = 2 * c;
-            at = to;
+        for (int c = cut; c < W; ++c) {
+            const int4 at = s_pos[c - cut + 1];
+            if (at.w == 0 || !same_item(at, x)) break;
+            if (before(at, s_pos[c - cut + 2])) s_slot[n++] = 2 * c;
         }
         s_n = n;
     }
+    Request r;
+    if (read_request(p, x.x, r) != 1) return;         // the same for all
     __syncthreads();
-    const int n = s_n, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (int q = blockIdx.y * (kCombineThreads / 32) + warp; q < rows; q += kCombineGroups * (kCombineThreads / 32)) {
-        const int tok = q / p.G, g = q - tok * p.G, half = ntok > p.tb && tok >= p.tb ? 1 : 0;
-        const int row = half * kTRows + (tok - half * p.tb) * p.G + g;
+    const int n = s_n, first = x.z * 2 * p.tb, ntok = min(2 * p.tb, r.T - first), rows = ntok * p.G;
+    const int lane = threadIdx.x % kRowLanes;
+    for (int q = blockIdx.y * ROWS + threadIdx.x / kRowLanes; q < rows; q += kCombineGroups * ROWS) {
+        // row q: its token and head, and its place among the parts' rows
+        const int half = ntok > p.tb && q >= p.tb * p.G ? 1 : 0, in_half = q - half * p.tb * p.G;
+        const int tok_in = (in_half * p.g_inv) >> 16, g = in_half - tok_in * p.G, tok = half * p.tb + tok_in;
+        const size_t row = (size_t)(half * kTRows + in_half);
         float m = -INFINITY;
-        for (int c = lane; c < n; c += 32) {
-            const float2 ml = p.part_ml[(size_t)s_slot[c] * 2 * kTRows + row];
-            s_w[warp][c] = ml;
-            m = fmaxf(m, ml.x);
-        }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        __syncwarp();
+        for (int c = 0; c < n; ++c) m = fmaxf(m, p.part_ml[(size_t)s_slot[c] * 2 * kTRows + row].x);
         float l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 4
+#pragma unroll 2
         for (int c = 0; c < n; ++c) {
-            const float2 ml = s_w[warp][c];
+            const size_t at = (size_t)s_slot[c] * 2 * kTRows + row;
+            const float2 ml = p.part_ml[at];
             const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-            const float* src = p.part_o + ((size_t)s_slot[c] * 2 * kTRows + row) * D + lane * E;
             float v[E];
-            if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(src);
-            else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(src);
+#pragma unroll
+            for (int e = 0; e < E; e += 4)
+                *reinterpret_cast<float4*>(&v[e]) = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * E + e);
             l = fmaf(f, ml.y, l);
 #pragma unroll
             for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
         }
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        uint32_t w[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2) w[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
         __nv_bfloat16* dst = p.out + (((size_t)r.row0 + first + tok) * p.Hq + (size_t)x.y * p.G + g) * D + lane * E;
-        if (E == 4)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[E - 2] * inv, acc[E - 1] * inv));
-        else
-            *reinterpret_cast<uint32_t*>(dst) = pack_bf16(acc[0] * inv, acc[1] * inv);
-        __syncwarp();
+        if (E == 8) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(w);
+        else *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(w);
     }
 }
 

@@ -66,6 +66,9 @@ struct TreeAttnParams {
     float scale_log2;             // log2(e) / sqrt(d)
     int batch, bt_stride, Hq, Hkv, G, P, num_pages, mask_words, n_tokens;
     int tb;                       // new tokens in the 128 rows of a stream: 128 / G
+    int g_inv;                    // 65536 / G + 1: x / G = (x g_inv) >> 16 for x < 256
+    unsigned long long two_inv;   // 2^37 / (2 tb) rounded up: x / (2 tb) = (x two_inv) >> 37 for x < 2^29
+    unsigned long long run_inv;   // 2^64 / runs
 };
 constexpr int kTreeRows = 128;
 constexpr int kMaxTreeRuns = 256; // CTAs of the attention at most
