@@ -27,8 +27,8 @@
 // unnormalised O, m and l go to the workspace and are merged by tree_combine
 // in a fixed order.  Nothing waits for another CTA.
 //
-// Warps: 0 loads Q and K (TMA), 2 loads V, 1 issues the MMAs, 4 .. 11 softmax
-// and output, one thread per row; for E4M3 pools 12 .. 19 turn the codes into
+// Warps: 0 and 2 load Q, K and V (TMA), 1 issues the MMAs, 4 .. 11 softmax and
+// output, one thread per row; for E4M3 pools 12 .. 19 turn the codes into
 // bf16 tiles (exact; the scales of a page and head go into the scores and the
 // weights in fp32).  P is rounded to bf16 for the matrix product, each weight off by at
 // most 2^-8 of itself; two terms of bf16 would cost half as much again on the
@@ -56,10 +56,6 @@ constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // times the mean.
 constexpr int kCostRowShift = 2, kCostKeyShift = 1, kCostItem = 9;
 constexpr int kCostRow = 1 << kCostRowShift, kCostKey = 1 << kCostKeyShift;
-#ifndef PKV_TREE_POLY
-#define PKV_TREE_POLY 2
-#endif
-constexpr int kPoly = PKV_TREE_POLY;          // of every 8 pairs of weights, those whose 2^x goes to the FMA pipe
 constexpr int kSnap = 2;                      // a cut this near to an item's ends moves there
 
 template <int D, bool FP8>
@@ -198,8 +194,13 @@ struct Walk {
 // 2 in key mode, tile u / 2 of stream u % 2 in row mode; the MMAs go S(0),
 // S(1), then P V(u), S(u + 2) for every u, and the loads in the order of
 // their first use.
-__device__ __forceinline__ int k_seq(const Segment& s, int i) { return s.row_mode ? 2 * i : i < 2 ? i : 2 * i - 1; }
-__device__ __forceinline__ int v_seq(const Segment& s, int i) { return s.row_mode ? 2 * i + 1 : i + min(i + 2, s.n); }
+__device__ __forceinline__ int lead_of(const Segment& s) { return s.row_mode ? 1 : 2; }   // K tiles before the first V
+__device__ __forceinline__ int k_seq(const Segment& s, int i)
+{
+    const int lead = lead_of(s);
+    return i < lead ? i : 2 * i - lead + 1;
+}
+__device__ __forceinline__ int v_seq(const Segment& s, int i) { return i + min(i + lead_of(s), s.n); }
 
 __device__ __forceinline__ void sts128(uint32_t addr, uint4 v)
 {
@@ -242,32 +243,6 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b)
-{
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
-// 2^z of a pair on the FMA pipe, z at most 8: the whole number n nearest z by
-// adding and taking away 1.5 2^23 (its low bits are then those of the sum), 2^(z
-// - n) by a polynomial of degree 3 (minimax in the relative error on [-1/2,
-// 1/2], found by Remez exchange: 7.5e-5, far below the 2^-8 of the bf16 that the
-// weight becomes), n added to the exponent.  Below 2^-126 it stays there: a row
-// that sees nothing is told by its reference, -inf, not by its sum.
-__device__ __forceinline__ uint64_t exp2_poly(uint64_t z)
-{
-    constexpr float kShift = 12582912.f;
-    z = two(max_nan(first_of(z), -126.f), max_nan(second_of(z), -126.f));
-    const uint64_t t = add2(z, two(kShift, kShift));
-    const uint64_t x = fma2(add2(t, two(-kShift, -kShift)), two(-1.f, -1.f), z);
-    uint64_t y = fma2(x, two(0.05517166852951f, 0.05517166852951f), two(0.24261112511158f, 0.24261112511158f));
-    y = fma2(x, y, two(0.69326096773148f, 0.69326096773148f));
-    y = fma2(x, y, two(0.99992805719376f, 0.99992805719376f));
-    return two(__uint_as_float((uint32_t)y + ((uint32_t)t << 23)),
-               __uint_as_float((uint32_t)(y >> 32) + ((uint32_t)(t >> 32) << 23)));
-}
-
 // The scores of keys that the row does not see become -inf, whatever they
 // were (of tiles with drafted keys, or pages out of range, before the pass
 // below: masks in that pass would double its code for one tile in many).
@@ -373,7 +348,7 @@ __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool 
             for (int i = 0; i < 8; ++i) {
                 const int c = 16 * h + 2 * i;
                 const uint64_t z = fma2(two(__uint_as_float(x[c]), __uint_as_float(x[c + 1])), f2, m2);
-                uint64_t e = i % 8 < kPoly ? exp2_poly(z) : two(ex2(first_of(z)), ex2(second_of(z)));
+                uint64_t e = two(ex2(first_of(z)), ex2(second_of(z)));
                 sum[i & 1] = add2(sum[i & 1], e);
                 if (FP8) e = mul2(e, two(vs[h], vs[h]));       // the V scale goes into what P V takes, not into the sum
                 w[i] = pack_bf16(first_of(e), second_of(e));
@@ -524,181 +499,189 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
     // E4M3: 640 threads of 96 registers at the start; the softmax takes what the
     // others do not need (144 x 256 + 64 x 384 = 96 x 640)
     if (warp < 4) {
-    if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    if (warp == 0 || warp == 2) {
-        // ---- loads: warp 0 those of Q and K, warp 2 those of V (a box takes
-        // about 100 cycles to issue; one warp alone was what bounded pages of
-        // 16 tokens)
-        const bool is_v = warp != 0;
-        const CUtensorMap* const map = is_v ? &tmv : &tmk;
-        constexpr int N = FP8 ? NCX : NS;
-        constexpr int ROWB = FP8 ? D : 2 * D;                // bytes of a row in the pool
-        const uint32_t lfull = FP8 ? cfull : full, lempty = FP8 ? cempty : empty, dst0 = FP8 ? stage : ring;
-        constexpr int LSLOT = FP8 ? Gm::STG : SLOT;
-        constexpr int LB = FP8 ? 1 : KB;                     // TMA boxes across a row
-        const int ppt = kTKeys / p.P;
-        int rb = 0, qc0 = 0, qc1 = 0, qsel = 0;
-        bool ok = true;
-        auto wait = [&](uint32_t bar, int phase) {
-            ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
-        };
-        while (ok && walk.next(p, s)) {
-            const int n_keys = s.L + s.T;
-            const int32_t* bt = p.block_tables + (size_t)s.b * p.bt_stride;
-            auto page_of = [&](int i) {                      // this lane's page of tile i; -1: out of range, -2: none
-                const int at = (s.t0 + i) * ppt + lane;
-                if (i >= s.n || lane >= ppt || at * p.P >= n_keys) return -2;
-                const int page = __ldg(&bt[at]);
-                return (unsigned)page < (unsigned)p.num_pages ? page : -1;
+        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == 0 || warp == 2) {
+            // ---- loads, in the order of their use, by warps 0 and 2 (a box takes
+            // about 100 cycles to issue: one warp alone was what bounded pages of
+            // 16 tokens).  bf16: warp 0 those of Q and K, warp 2 those of V.  E4M3:
+            // each issues every other box of every load (183 us; by K and V 198).
+            // A warp waits for its own places only.  A parity tells two phases
+            // apart, so that needs its last place within a ring before the next
+            // one: they are at most 3 apart.
+            const int half = warp >> 1;
+            constexpr int N = FP8 ? NCX : NS;
+            constexpr int ROWB = FP8 ? D : 2 * D;                // bytes of a row in the pool
+            const uint32_t lfull = FP8 ? cfull : full, lempty = FP8 ? cempty : empty, dst0 = FP8 ? stage : ring;
+            constexpr int LSLOT = FP8 ? Gm::STG : SLOT;
+            constexpr int LB = FP8 ? 1 : KB;                     // TMA boxes across a row
+            const int ppt = kTKeys / p.P;
+            int rb = 0, qc0 = 0, qc1 = 0, qsel = 0;
+            bool ok = true;
+            auto wait = [&](uint32_t bar, int phase) {
+                ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
             };
-            auto load_q = [&](int buf, int& count, int token) {
-                if (count > 0) wait(qempty + 8u * buf, count - 1);
-                if (!ok) return;
-                if (elect_one()) {
-                    s_issued[kMaxSlots + buf] = count + 1;
-                    mbar_arrive_expect_tx(qfull + 8u * buf, (uint32_t)(KB * 128 * p.tb * p.G));
-#pragma unroll
-                    for (int kb = 0; kb < KB; ++kb)
-                        tma_load_3d(q0 + (uint32_t)(buf * SLOT + kb * kTBlk), &tmq, 64 * kb, s.kvh * p.G, token, qfull + 8u * buf);
-                }
-                __syncwarp();
-                ++count;
-            };
-            int page = page_of(0);
-            for (int i = 0; ok && i < s.n; ++i) {
-                const int cur = page;
-                page = page_of(i + 1);
-                const int seq = rb + (is_v ? v_seq(s, i) : k_seq(s, i)), j = seq % N;
-                if (seq >= N) wait(lempty + 8u * j, seq / N - 1);
-                if (!ok) break;
-                if (cur == -1) {                             // its keys are masked; an in-range page keeps the copy legal
-                    s_bad = 1;
-                    atomicOr(p.err, kErrPage);
-                }
-                const int np = __popc(__ballot_sync(0xffffffffu, cur != -2));
-                const int y = (max(cur, 0) * p.Hkv + s.kvh) * p.P;
-                if (elect_one()) {
-                    s_issued[j] = seq / N + 1;
-                    mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
-                }
-                uint32_t dst = dst0 + (uint32_t)(j * LSLOT);
-                for (int k = 0; k < np; ++k) {
-                    const int yk = __shfl_sync(0xffffffffu, y, k);
+            while (ok && walk.next(p, s)) {
+                const int n_keys = s.L + s.T;
+                const int32_t* bt = p.block_tables + (size_t)s.b * p.bt_stride;
+                auto page_of = [&](int i) {                      // this lane's page of tile i; -1: out of range, -2: none
+                    const int at = (s.t0 + i) * ppt + lane;
+                    if (i >= s.n || lane >= ppt || at * p.P >= n_keys) return -2;
+                    const int page = __ldg(&bt[at]);
+                    return (unsigned)page < (unsigned)p.num_pages ? page : -1;
+                };
+                auto load_q = [&](int buf, int& count, int token) {
+                    if (count > 0) wait(qempty + 8u * buf, count - 1);
+                    if (!ok) return;
                     if (elect_one()) {
+                        s_issued[kMaxSlots + buf] = count + 1;
+                        mbar_arrive_expect_tx(qfull + 8u * buf, (uint32_t)(KB * 128 * p.tb * p.G));
 #pragma unroll
-                        for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * kTBlk), map, 64 * kb, yk, lfull + 8u * j);
+                        for (int kb = 0; kb < KB; ++kb)
+                            tma_load_3d(q0 + (uint32_t)(buf * SLOT + kb * kTBlk), &tmq, 64 * kb, s.kvh * p.G, token, qfull + 8u * buf);
                     }
-                    dst += (uint32_t)(p.P * (FP8 ? D : 128));
-                }
-                __syncwarp();
-                if (!is_v && i == 0) {                       // the first tile is under way: now Q, once it is free
-                    if (s.row_mode) {
-                        load_q(0, qc0, s.row0);
-                        load_q(1, qc1, s.row0 + p.tb);
-                    } else {
-                        if (qsel == 0) load_q(0, qc0, s.row0);
-                        else load_q(1, qc1, s.row0);
-                        qsel ^= 1;
-                    }
-                }
-            }
-            rb += 2 * s.n;
-        }
-        if (!ok) s_fail = 1;
-    } else if (warp == 1) {
-        // ---- MMA issue: the warp together, one elected lane for each instruction
-        constexpr uint32_t idS = umma_idesc_bf16<kTRows, kTKeys>();
-        constexpr uint32_t idO = umma_idesc_bf16<kTRows, D, true>();
-        int rb = 0, qsel = 0, qc0 = 0, qc1 = 0, pc0 = 0, pc1 = 0;
-        bool ok = true;
-        auto wait = [&](uint32_t bar, int phase) {
-            ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
-        };
-        while (ok && walk.next(p, s)) {
-            const int qb0 = s.row_mode ? 0 : qsel, qb1 = s.row_mode ? 1 : qsel;
-            auto tile_of = [&](int u) { return s.row_mode ? u >> 1 : u; };
-            auto k_bar = [&](int u, int& phase) {
-                const int seq = rb + k_seq(s, tile_of(u));
-                phase = seq / NS;
-                return seq % NS;
-            };
-            // the instructions of S(u), by the elected lane
-            auto score = [&](int u, int slot) {
-                const int st = u & 1, qb = st ? qb1 : qb0;
-                const uint64_t qa = sw128_kmajor_desc(q0 + (uint32_t)(qb * SLOT)),
-                               ka = sw128_kmajor_desc(ring + (uint32_t)(slot * SLOT));
-                const uint32_t dcol = tmem + (uint32_t)(st * kTKeys);
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint64_t off = (uint64_t)(((kk >> 2) * kTBlk + (kk & 3) * 32) >> 4);
-                    umma_bf16_all(dcol, qa + off, ka + off, idS, kk ? 1u : 0u);
-                }
-                umma_commit(sfull + 8u * st);
-                if (!s.row_mode || st) umma_commit(empty + 8u * slot);
-                if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) umma_commit(qempty + 8u * qb);
-            };
-            wait(qfull + 8u * qb0, qb0 ? qc1 : qc0);
-            if (s.row_mode) wait(qfull + 8u, qc1);
-            if (s.row_mode || qb0) ++qc1;
-            if (s.row_mode || !qb0) ++qc0;
-            for (int u = 0; u < 2 && u < s.units; ++u) {
-                int phase;
-                const int slot = k_bar(u, phase);
-                wait(full + 8u * slot, phase);
-                if (!ok) break;
-                tmem_fence_after();
-                if (elect_one()) score(u, slot);
-                __syncwarp();
-            }
-            // P V(u) and S(u + 2) go out together once P(u) is written; that K
-            // has landed is looked at while P is awaited
-            for (int u = 0; ok && u < s.units; ++u) {
-                const int st = u & 1, i = tile_of(u);
-                const int vseq = rb + v_seq(s, i), vslot = vseq % NS;
-                const bool next = u + 2 < s.units;
-                int kphase = 0, kslot = 0;
-                if (next) kslot = k_bar(u + 2, kphase);
-                wait(full + 8u * vslot, vseq / NS);
-                const bool k_here = next && __all_sync(0xffffffffu, mbar_try_wait(full + 8u * kslot, (uint32_t)(kphase & 1)));
-                const int steps = (min(kTKeys, s.L + s.T - (s.t0 + i) * kTKeys) + 15) / 16;
-                const uint64_t va = sw128_mnmajor_desc(ring + (uint32_t)(vslot * SLOT), (uint32_t)kTBlk, 1024u);
-                const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
-                const uint32_t later = u >= 2 ? 1u : 0u;
-                wait(pfull + 8u * st, st ? pc1 : pc0);
-                if (st) ++pc1;
-                else ++pc0;
-                if (!ok) break;
-                tmem_fence_after();
-                if (elect_one()) {
-                    if (steps == kTKeys / 16) {
-#pragma unroll
-                        for (int kk = 0; kk < kTKeys / 16; ++kk)        // 16 keys each
-                            umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
-                    } else {
-#pragma unroll 1
-                        for (int kk = 0; kk < steps; ++kk)
-                            umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
-                    }
-                    if (!s.row_mode || st) umma_commit(empty + 8u * vslot);
-                    if (!next) umma_commit(ofin + 8u * st);
-                    if (k_here) score(u + 2, kslot);
-                }
-                __syncwarp();
-                if (next && !k_here) {
-                    wait(full + 8u * kslot, kphase);
+                    __syncwarp();
+                    ++count;
+                };
+                const int lead = lead_of(s);
+                int ik = 0, iv = 0, kpage = page_of(0), vpage = kpage;
+                while (ok) {
+                    const bool is_k = FP8 ? ik < s.n && ik < iv + lead : half == 0;
+                    if ((is_k ? ik : iv) >= s.n) break;
+                    const int seq = rb + (is_k ? k_seq(s, ik) : v_seq(s, iv)), cur = is_k ? kpage : vpage;
+                    if (is_k) kpage = page_of(++ik);
+                    else vpage = page_of(++iv);
+                    const int j = seq % N;
+                    if (seq >= N) wait(lempty + 8u * j, seq / N - 1);
                     if (!ok) break;
-                    if (elect_one()) score(u + 2, kslot);
+                    if (cur == -1) {                             // its keys are masked; an in-range page keeps the copy legal
+                        s_bad = 1;
+                        atomicOr(p.err, kErrPage);
+                    }
+                    const int np = __popc(__ballot_sync(0xffffffffu, cur != -2));
+                    const int y = (max(cur, 0) * p.Hkv + s.kvh) * p.P;
+                    if ((!FP8 || half == 0) && elect_one()) {
+                        s_issued[j] = seq / N + 1;
+                        mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
+                    }
+                    const CUtensorMap* const map = is_k ? &tmk : &tmv;
+                    uint32_t dst = dst0 + (uint32_t)(j * LSLOT);
+                    for (int k = 0; k < np; ++k) {
+                        const int yk = __shfl_sync(0xffffffffu, y, k);
+                        if ((!FP8 || (k & 1) == half) && elect_one()) {
+#pragma unroll
+                            for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * kTBlk), map, 64 * kb, yk, lfull + 8u * j);
+                        }
+                        dst += (uint32_t)(p.P * (FP8 ? D : 128));
+                    }
+                    __syncwarp();
+                    if (half == 0 && ik + iv == 1) {         // the first tile is under way: now Q, once it is free
+                        if (s.row_mode) {
+                            load_q(0, qc0, s.row0);
+                            load_q(1, qc1, s.row0 + p.tb);
+                        } else {
+                            if (qsel == 0) load_q(0, qc0, s.row0);
+                            else load_q(1, qc1, s.row0);
+                            qsel ^= 1;
+                        }
+                    }
+                }
+                rb += 2 * s.n;
+            }
+            if (!ok) s_fail = 1;
+        } else if (warp == 1) {
+            // ---- MMA issue: the warp together, one elected lane for each instruction
+            constexpr uint32_t idS = umma_idesc_bf16<kTRows, kTKeys>();
+            constexpr uint32_t idO = umma_idesc_bf16<kTRows, D, true>();
+            int rb = 0, qsel = 0, qc0 = 0, qc1 = 0, pc0 = 0, pc1 = 0;
+            bool ok = true;
+            auto wait = [&](uint32_t bar, int phase) {
+                ok = ok && __all_sync(0xffffffffu, wait_bar(bar, (uint32_t)(phase & 1))) != 0;
+            };
+            while (ok && walk.next(p, s)) {
+                const int qb0 = s.row_mode ? 0 : qsel, qb1 = s.row_mode ? 1 : qsel;
+                auto tile_of = [&](int u) { return s.row_mode ? u >> 1 : u; };
+                auto k_bar = [&](int u, int& phase) {
+                    const int seq = rb + k_seq(s, tile_of(u));
+                    phase = seq / NS;
+                    return seq % NS;
+                };
+                // the instructions of S(u), by the elected lane
+                auto score = [&](int u, int slot) {
+                    const int st = u & 1, qb = st ? qb1 : qb0;
+                    const uint64_t qa = sw128_kmajor_desc(q0 + (uint32_t)(qb * SLOT)),
+                                   ka = sw128_kmajor_desc(ring + (uint32_t)(slot * SLOT));
+                    const uint32_t dcol = tmem + (uint32_t)(st * kTKeys);
+#pragma unroll
+                    for (int kk = 0; kk < D / 16; ++kk) {
+                        const uint64_t off = (uint64_t)(((kk >> 2) * kTBlk + (kk & 3) * 32) >> 4);
+                        umma_bf16_all(dcol, qa + off, ka + off, idS, kk ? 1u : 0u);
+                    }
+                    umma_commit(sfull + 8u * st);
+                    if (!s.row_mode || st) umma_commit(empty + 8u * slot);
+                    if (s.row_mode ? u >= s.units - 2 : u == s.units - 1) umma_commit(qempty + 8u * qb);
+                };
+                wait(qfull + 8u * qb0, qb0 ? qc1 : qc0);
+                if (s.row_mode) wait(qfull + 8u, qc1);
+                if (s.row_mode || qb0) ++qc1;
+                if (s.row_mode || !qb0) ++qc0;
+                for (int u = 0; u < 2 && u < s.units; ++u) {
+                    int phase;
+                    const int slot = k_bar(u, phase);
+                    wait(full + 8u * slot, phase);
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (elect_one()) score(u, slot);
                     __syncwarp();
                 }
+                // P V(u) and S(u + 2) go out together once P(u) is written; that K
+                // has landed is looked at while P is awaited
+                for (int u = 0; ok && u < s.units; ++u) {
+                    const int st = u & 1, i = tile_of(u);
+                    const int vseq = rb + v_seq(s, i), vslot = vseq % NS;
+                    const bool next = u + 2 < s.units;
+                    int kphase = 0, kslot = 0;
+                    if (next) kslot = k_bar(u + 2, kphase);
+                    wait(full + 8u * vslot, vseq / NS);
+                    const bool k_here = next && __all_sync(0xffffffffu, mbar_try_wait(full + 8u * kslot, (uint32_t)(kphase & 1)));
+                    const int steps = (min(kTKeys, s.L + s.T - (s.t0 + i) * kTKeys) + 15) / 16;
+                    const uint64_t va = sw128_mnmajor_desc(ring + (uint32_t)(vslot * SLOT), (uint32_t)kTBlk, 1024u);
+                    const uint32_t pcol = tmem + (uint32_t)(st * kTKeys), ocol = tmem + kTOcol + (uint32_t)(st * 128);
+                    const uint32_t later = u >= 2 ? 1u : 0u;
+                    wait(pfull + 8u * st, st ? pc1 : pc0);
+                    if (st) ++pc1;
+                    else ++pc0;
+                    if (!ok) break;
+                    tmem_fence_after();
+                    if (elect_one()) {
+                        if (steps == kTKeys / 16) {
+#pragma unroll
+                            for (int kk = 0; kk < kTKeys / 16; ++kk)        // 16 keys each
+                                umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                        } else {
+#pragma unroll 1
+                            for (int kk = 0; kk < steps; ++kk)
+                                umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                        }
+                        if (!s.row_mode || st) umma_commit(empty + 8u * vslot);
+                        if (!next) umma_commit(ofin + 8u * st);
+                        if (k_here) score(u + 2, kslot);
+                    }
+                    __syncwarp();
+                    if (next && !k_here) {
+                        wait(full + 8u * kslot, kphase);
+                        if (!ok) break;
+                        if (elect_one()) score(u + 2, kslot);
+                        __syncwarp();
+                    }
+                }
+                if (!s.row_mode) qsel ^= 1;
+                rb += 2 * s.n;
             }
-            if (!s.row_mode) qsel ^= 1;
-            rb += 2 * s.n;
+            if (!ok) s_fail = 1;
+            if (elect_one()) umma_commit(drain);                   // every MMA has ended before the tensor memory is given back
+            (void)mbar_wait_bounded(drain, 0u, kTWaitNs);
+            __syncwarp();
         }
-        if (!ok) s_fail = 1;
-        if (elect_one()) umma_commit(drain);                   // every MMA has ended before the tensor memory is given back
-        (void)mbar_wait_bounded(drain, 0u, kTWaitNs);
-        __syncwarp();
-    }
     } else if (warp < 12) {
         if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
         // ---- softmax and output: row r of stream st
