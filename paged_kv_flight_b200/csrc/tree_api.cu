@@ -145,6 +145,7 @@ pkv_status pkv_rope_append_axes(pkv_ctx* ctx, const void* q, const void* k_new, 
     p.Hq = c.num_q_heads;
     p.Hkv = c.num_kv_heads;
     p.P = c.page_size;
+    p.page_shift = page_shift(p.P);
     p.num_pages = c.num_pages;
     p.n_axes = n_axes;
     p.interleaved = interleaved != 0;

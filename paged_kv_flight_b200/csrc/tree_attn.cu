@@ -1047,7 +1047,10 @@ cudaError_t launch_t(const TreeAttnParams& p, const CUtensorMap& tmq, const CUte
 {
     tree_attn_kernel<D, FP8><<<runs, TreeGeo<D, FP8>::THREADS, TreeGeo<D, FP8>::BYTES, stream>>>(tmq, tmk, tmv, p);
     cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || runs < 2) return e;
+    // tables of up to 2 kSnap + 1 tiles: every cut lies near an item's end and
+    // has moved there, so that nothing is left to merge (4 requests, 14.0 us a
+    // call with the launch, 12.3 without)
+    if (e != cudaSuccess || runs < 2 || (long long)p.bt_stride * p.P <= (2 * kSnap + 1) * kTKeys) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(runs - 1), kCombineGroups);
     cfg.blockDim = dim3(kCombineThreads);

@@ -42,7 +42,7 @@ struct RopeAxesParams {
     const float* v_scale;
     const double* theta;          // [D / 2] rope_base^(-2i/D) in fp64, from the context
     int* err;
-    int n_tokens, Hq, Hkv, P, num_pages;
+    int n_tokens, Hq, Hkv, P, page_shift, num_pages;
     int n_axes, interleaved;
     int bound[kMaxAxes];          // consecutive: the first pair past axis a; interleaved: n_axes * sections[a]
 };
