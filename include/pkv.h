@@ -77,7 +77,9 @@
  * than bt_stride * P) skip the affected request or tile and set a sticky
  * device error word, which pkv_check_device_error reads; no call traps.  The
  * four calls of the tree step also want the context's device to be current
- * (PKV_ERR_INVALID_ARG otherwise).
+ * (PKV_ERR_INVALID_ARG otherwise), and take requests of at most 2^31 - 256
+ * tokens and, where masks or slots are planned or read, fewer than 2^29 rows
+ * (PKV_ERR_UNSUPPORTED).
  * C++ exceptions never cross this ABI.
  */
 #ifndef PKV_H
@@ -383,8 +385,11 @@ pkv_status pkv_rope_append_axes(pkv_ctx* ctx, const void* q, const void* k_new, 
  *   q, out     [n_tokens][Hq][d] bf16; rows outside every request are left
  *              as they were.  q and out may not overlap.
  *   tree_mask  [n_tokens][mask_words] 32-bit words, T_b <= 32 mask_words
- * bf16 or E4M3 pools (scales as for pkv_decode_attn).  The cache is read once
- * for every 2 * (128 / G) new tokens of a request.  The work is split over
+ * bf16 or E4M3 pools (scales as for pkv_decode_attn, finite).  The cache is read
+ * once for every 2 * (128 / G) new tokens of a request.  Weights are rounded to
+ * bf16 for the product with V (2^-8 of each at most), sums are fp32.  What K and V
+ * of new tokens hold that a row does not see, NaN and infinity included, does not
+ * touch the row.  The work is split over
  * the SMs along the cache, and partial results are merged by log-sum-exp in a
  * fixed order: results repeat bit for bit.  A request with lengths out of
  * range, or more than 32 mask_words new tokens, gets zeros and sets the error

@@ -48,7 +48,7 @@ __device__ __forceinline__ Request read_request(const SlotMapParams& p, int b)
     r.L = p.seq_lens[b];
     r.n = p.new_lens[b];
     r.held = p.pages_held[b];
-    const long long L = r.L, n = r.n, cap = (long long)p.bt_stride * p.P;
+    const long long L = r.L, n = r.n, cap = min((long long)p.bt_stride * p.P, kMaxTreeKeys);
     r.ok = L >= 0 && n >= 0 && r.held >= 0 && r.held <= p.bt_stride && (long long)r.held * p.P >= L && L + n <= cap &&
            !(p.parents && n > 32ll * p.mask_words);
     if (r.n < 0) r.n = 0;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
                 const int b = l, start = s_cu[b], i = row - start, L = p.seq_lens[b], held = p.pages_held[b];
                 const int first = s_first[b];
                 const bool in_range = first >= 0 || read_request(p, b).ok;
-                const int at = (int)min((long long)L + i, (long long)p.bt_stride * p.P - 1);
+                const int at = (int)min((long long)L + i, kMaxTreeKeys);      // of a request in range: L + i
                 const int lp = max(at, 0) >> p.page_shift, place = at & (p.P - 1);
                 int page = -1;
                 if (first >= 0)

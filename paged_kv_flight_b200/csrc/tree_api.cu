@@ -10,6 +10,9 @@ namespace {
 
 using pkv::aligned16;
 
+// Rows of a call: the kernels' row counters and reciprocals.
+constexpr int kMaxRows = (1 << 29) - 1;
+
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Whether [a, a + an) and [b, b + bn) share a byte.
@@ -42,6 +45,7 @@ pkv_status pkv_slot_map(pkv_ctx* ctx, const int32_t* seq_lens, const int32_t* ne
                         int32_t* positions, uint32_t* tree_mask, cudaStream_t stream)
 {
     if (!ctx || batch < 0 || batch > ctx->cfg.max_batch || n_tokens < 0 || free_cap < 0) return PKV_ERR_INVALID_ARG;
+    if (n_tokens > kMaxRows) return PKV_ERR_UNSUPPORTED;
     if (batch == 0) return PKV_OK;
     if (bt_stride <= 0 || bt_stride > ctx->cfg.max_blocks_per_seq) return PKV_ERR_INVALID_ARG;
     if (!seq_lens || !new_lens || !block_tables || !pages_held || !pages_out || !free_count || !free_left || !cu_q ||
@@ -162,6 +166,7 @@ pkv_status pkv_decode_attn_tree(pkv_ctx* ctx, const void* q, const void* k_pool,
         pkv::check_call(ctx, batch, bt_stride, k_pool, v_pool, k_scale, v_scale, block_tables, seq_lens);
     if (st != PKV_OK) return st;
     if (n_tokens < 0) return PKV_ERR_INVALID_ARG;
+    if (n_tokens > kMaxRows) return PKV_ERR_UNSUPPORTED;
     if (batch == 0 || n_tokens == 0) return PKV_OK;
     if (!q || !out || !cu_q || !tree_mask || mask_words <= 0) return PKV_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(out) || !aligned16(cu_q) || !aligned4(tree_mask)) return PKV_ERR_INVALID_ARG;
@@ -169,7 +174,6 @@ pkv_status pkv_decode_attn_tree(pkv_ctx* ctx, const void* q, const void* k_pool,
     if (overlap(q, bytes, out, bytes)) return PKV_ERR_INVALID_ARG;
     const pkv_status dev = check_device(ctx);
     if (dev != PKV_OK) return dev;
-    if (n_tokens >= 1 << 29) return PKV_ERR_UNSUPPORTED;      // the kernel's reciprocals
 
     const int tb = pkv::kTreeRows / ctx->G;
     if (!pkv::page_maps(ctx, k_pool, v_pool)) return PKV_ERR_CUDA;

@@ -95,7 +95,7 @@ __device__ __forceinline__ int read_request(const TreeAttnParams& p, int b, Requ
     r.T = e - a;
     if (r.T == 0) return 0;
     const long long keys = (long long)r.L + r.T;
-    if (r.L < 0 || keys > (long long)p.bt_stride * p.P || r.T > 32ll * p.mask_words) return 3;
+    if (r.L < 0 || keys > min((long long)p.bt_stride * p.P, kMaxTreeKeys) || r.T > 32ll * p.mask_words) return 3;
     r.NT = (int)((keys + kTKeys - 1) / kTKeys);
     return 1;
 }
@@ -553,12 +553,12 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     const int j = seq % N;
                     if (seq >= N) wait(lempty + 8u * j, seq / N - 1);
                     if (!ok) break;
-                    if (cur == -1) {                             // its keys are masked; an in-range page keeps the copy legal
+                    if (cur == -1) {                             // its keys are masked, and rows above the pool read as zero
                         s_bad = 1;
                         atomicOr(p.err, kErrPage);
                     }
                     const int np = __popc(__ballot_sync(0xffffffffu, cur != -2));
-                    const int y = (max(cur, 0) * p.Hkv + s.kvh) * p.P;
+                    const int y = cur < 0 ? -p.P : (cur * p.Hkv + s.kvh) * p.P;
                     if ((!FP8 || half == 0) && elect_one()) {
                         s_issued[j] = seq / N + 1;
                         mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
@@ -756,7 +756,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
 #pragma unroll
                             for (int w = 0; w < 4; ++w) {          // the page's keys: 16 or 32 bits of a word, or two words
                                 const int c = (k << shift) - 32 * w;
-                                if (c > -32 && c < 32) vis[w] &= ~((shift == 4 ? 0xFFFFu : 0xFFFFFFFFu) << max(c, 0));
+                                if (c > -p.P && c < 32) vis[w] &= ~((shift == 4 ? 0xFFFFu : 0xFFFFFFFFu) << max(c, 0));
                             }
                         }
                         tile_mask(scol, vis);

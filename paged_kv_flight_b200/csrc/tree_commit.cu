@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeC
     int a = tid < p.path_stride ? __ldg(&path[tid]) : 0;    // on its way with the lengths
     int before = tid > 0 && tid < p.path_stride ? __ldg(&path[tid - 1]) : -1;
     const int L = p.seq_lens[b], n = p.path_lens[b];
-    const long long cap = (long long)p.bt_stride * p.P;
+    const long long cap = min((long long)p.bt_stride * p.P, kMaxTreeKeys);
     int bad = L < 0 || n < 0 || n > p.path_stride || (long long)L + n > cap ? kErrLength : 0;
     if (!bad) {
         for (int j = tid; j < n; j += kCommitThreads) {

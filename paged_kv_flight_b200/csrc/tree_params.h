@@ -7,6 +7,9 @@
 
 namespace pkv {
 
+// Largest cached and new tokens of a request: places in it are 32-bit.
+constexpr long long kMaxTreeKeys = 0x7FFFFF00;
+
 struct SlotMapParams {
     const int32_t* seq_lens;
     const int32_t* new_lens;

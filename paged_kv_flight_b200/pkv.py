@@ -531,10 +531,19 @@ def _act(x, shape, name):
 
 
 def _sizes(x, n, name):
-    """The sizes of a tensor of n dimensions."""
+    """The sizes of a tensor of n dimensions (the calls of the tree step take
+    their sizes from some of their arguments: these are tensors, not raw
+    pointers)."""
     if not isinstance(x, _Tensor) or x.dim() != n:
         raise ValueError(f"{name}: expected a tensor of {n} dimensions")
     return x.shape
+
+
+def _here(x, name):
+    """A call runs on the current device."""
+    d = x.get_device()
+    if d >= 0 and _cur_device is not None and d != _cur_device():
+        raise ValueError(f"{name}: on cuda:{d}, the current device is cuda:{_cur_device()}")
 
 
 def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, free_count, cu_q, slots, positions,
@@ -548,6 +557,7 @@ def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, 
     n, = _sizes(slots, 1, "slots")
     cap, = _sizes(free_pages, 1, "free_pages")
     words = 0 if tree_mask is None else _sizes(tree_mask, 2, "tree_mask")[1]
+    _here(block_tables, "block_tables")
     st = lib.pkv_slot_map(ctx, _vec(seq_lens, B, "seq_lens"), _vec(new_lens, B, "new_lens"),
                           None if parents is None else _vec(parents, n, "parents"), B,
                           _mat(block_tables, (B, stride), "block_tables"), stride, _vec(pages_held, B, "pages_held"),
@@ -568,6 +578,7 @@ def pkv_rope_append_axes(ctx, q, k_new, v_new, positions, sections, slots, q_out
     n, axes = q_shape[0], len(sections)
     if k_shape[0] != n or k_shape[2] != q_shape[2]:
         raise ValueError(f"k_new: shape {tuple(k_shape)} next to q of {tuple(q_shape)}")
+    _here(q, "q")
     st = lib.pkv_rope_append_axes(ctx, _act(q, q_shape, "q"), _act(k_new, k_shape, "k_new"),
                                   _act(v_new, k_shape, "v_new"), n, _mat(positions, (axes, n), "positions"), axes,
                                   (_I * axes)(*sections), 1 if interleaved else 0, _vec(slots, n, "slots"),
@@ -585,6 +596,7 @@ def pkv_decode_attn_tree(ctx, q, k_pool, v_pool, k_scale, v_scale, block_tables,
     B, stride = _sizes(block_tables, 2, "block_tables")
     words = _sizes(tree_mask, 2, "tree_mask")[1]
     n = q_shape[0]
+    _here(q, "q")
     st = lib.pkv_decode_attn_tree(ctx, _act(q, q_shape, "q"), *_kv(k_pool, v_pool, k_scale, v_scale),
                                   _mat(block_tables, (B, stride), "block_tables"), stride,
                                   _vec(seq_lens, B, "seq_lens"), _vec(cu_q, B + 1, "cu_q"),
@@ -599,6 +611,7 @@ def pkv_tree_commit(ctx, k_pool, v_pool, k_scale, v_scale, block_tables, seq_len
     new tokens of request b in rising order; lens_out [batch] may be seq_lens."""
     B, stride = _sizes(block_tables, 2, "block_tables")
     depth = _sizes(path, 2, "path")[1]
+    _here(block_tables, "block_tables")
     st = lib.pkv_tree_commit(ctx, *_kv(k_pool, v_pool, k_scale, v_scale),
                              _mat(block_tables, (B, stride), "block_tables"), stride, _vec(seq_lens, B, "seq_lens"),
                              _mat(path, (B, depth), "path"), depth, _vec(path_lens, B, "path_lens"), B,

@@ -770,3 +770,109 @@ def test_wrong_device_or_stream(pkv):
         side.synchronize()
         _ok(pkv, ctx)
         _attn_near(out, ref, size)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_attention_bad_page_next_to_nan(pkv, fp8):
+    """A page out of range is left out whatever the pool holds elsewhere."""
+    x = _attn_inputs((8, 2, 128, 16, fp8, [300], [5], "random"))
+    unused = int(np.setdiff1d(np.arange(x["pages"]), x["table"][0])[0])
+    for name in ("k", "v"):
+        u = x[name].view(torch.uint8) if fp8 else x[name]
+        swap = u[0].clone()                       # page 0 becomes nobody's, and no number
+        u[unused] = swap
+        u[0] = 0x7F if fp8 else float("nan")
+        if fp8:
+            x[name + "s"][unused] = x[name + "s"][0]
+        x[name + "v"][unused] = x[name + "v"][0]
+    x["table"][x["table"] == 0] = unused
+    kept = dict(x, table=np.concatenate([np.delete(x["table"][0], 3), x["table"][0][3:4]])[None], lens=x["lens"] - 16)
+    ref, size = _attn_ref(kept)
+    x["table"][0, 3] = -7
+    with _attn_ctx(pkv, x) as ctx:
+        out = _attn_run(pkv, ctx, _attn_device(x))
+        assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 2)
+        _attn_near(out, ref, size)
+
+
+def test_lengths_at_the_end_of_32_bits(pkv):
+    """Lengths whose sum with the new tokens passes 32 bits are out of range,
+    also under a table long enough for them."""
+    blocks = (1 << 25) - 1                                  # x 64 tokens: 2^31 - 64, the longest table a context takes
+    i = lambda *v: _i(np.array(v))   # noqa: E731
+    table = torch.zeros(1, blocks, dtype=torch.int32, device=DEV)
+    with _Ctx(pkv, 4, 1, 64, 64, False, 1, blocks, 4) as ctx:
+        pool = torch.zeros(4, 1, 64, 64, dtype=torch.bfloat16, device=DEV)
+        q = torch.ones(8, 4, 64, dtype=torch.bfloat16, device=DEV)
+        for L in (64 * blocks - 3, 2 ** 31 - 4, 2 ** 31 - 1):
+            out = torch.full_like(q, 7.0)
+            pkv.pkv_decode_attn_tree(ctx, q, pool, pool, None, None, table, i(L), i(0, 8),
+                                     torch.ones(8, 1, dtype=torch.int32, device=DEV), out)
+            assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 1) and (out == 0).all()
+            slots, pos, pages, left, cu = i(*[5] * 8), i(*[5] * 8), i(5), i(5), i(5, 5)
+            pkv.pkv_slot_map(ctx, i(L), i(8), table, i(blocks), i(1, 2), i(2), cu, slots, pos, pages, left)
+            assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 1)
+            assert (slots == -1).all() and int(pages[0]) == blocks and int(left[0]) == 2 and cu.tolist() == [0, 8]
+            lens = i(5)
+            pkv.pkv_tree_commit(ctx, pool, pool, None, None, table, i(L), i(1, 2, 3)[None], i(3), lens)
+            assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 1) and int(lens[0]) == L
+
+
+def test_offsets_past_32_bits(pkv):
+    """Pages at the far end of pools of more than 2^32 bytes and 2^31 elements:
+    the same bits as from pools that hold those pages alone."""
+    x = _attn_inputs((16, 8, 128, 64, False, [200, 70], [9, 20], "random"))
+    pages, n = 34000, x["pages"]                            # x 64 K elements
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("18 GB of pools")
+    far = dict(x, table=np.where(x["table"] >= 0, x["table"] + pages - n, -1).astype(np.int32))
+    g, f = _attn_device(x), None
+    with _attn_ctx(pkv, x) as ctx:
+        near = _attn_run(pkv, ctx, g)
+    small = {k: g[k].clone() for k in ("k", "v")}
+    big = {k: torch.zeros(pages, *x[k].shape[1:], dtype=torch.bfloat16, device=DEV) for k in ("k", "v")}
+    for k in big:
+        big[k][pages - n:] = small[k]
+    f = dict(_attn_device(dict(far, k=x["k"][:1], v=x["v"][:1])), **big)
+    Hq, Hkv, d, P = x["case"][:4]
+    kn = torch.randn(4, Hkv, d, device=DEV).to(torch.bfloat16)
+    qn = torch.randn(4, Hq, d, device=DEV).to(torch.bfloat16)
+    slots, pos = np.array([3, 64 * n - 1, 130, 400]), _i([[9, 70000, 3, 5]])
+    path, plen = _i([[1, 4, 8], [3, 5, 19]]), _i([3, 2])
+    got = {}
+    for name, pool, table, count, shift in (("near", small, x["table"], n, 0), ("far", big, far["table"], pages, pages - n)):
+        with _Ctx(pkv, Hq, Hkv, d, P, False, 2, x["table"].shape[1], count) as ctx:
+            if name == "far":
+                out = torch.empty_like(f["q"])
+                pkv.pkv_decode_attn_tree(ctx, f["q"], pool["k"], pool["v"], None, None, f["table"], f["lens"], f["cu"],
+                                         f["mask"], out)
+                assert torch.equal(out, near)
+            qo, lens = torch.empty_like(qn), _i([0, 0])
+            pkv.pkv_rope_append_axes(ctx, qn, kn, kn, pos, [64], _i(slots + 64 * shift), qo, pool["k"], pool["v"], None, None)
+            pkv.pkv_tree_commit(ctx, pool["k"], pool["v"], None, None, _i(table), f["lens"], path, plen, lens)
+            _ok(pkv, ctx)
+            got[name] = (qo, pool["k"][count - n:].clone(), pool["v"][count - n:].clone(), lens)
+    for a, b in zip(*got.values()):
+        assert torch.equal(a, b)
+    assert not big["k"][:pages - n].any() and not big["v"][:pages - n].any()
+
+
+def test_two_contexts_on_two_streams(pkv):
+    """Steps of two contexts in flight together do not touch one another."""
+    runs = []
+    for seed, case in ((0, (8, 2, 64, 16, False, [3000, 90], [12, 40], "random")),
+                       (1, (16, 2, 128, 32, True, [2500, 7], [30, 9], "random"))):
+        x = _attn_inputs(case, seed)
+        runs.append((x, _attn_device(x), _attn_ref(x), _attn_ctx(pkv, x), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+    for _ in range(20):
+        for o, (x, g, ref, ctx, stream) in zip(outs, runs):
+            with torch.cuda.stream(stream):
+                o.append(_attn_run(pkv, ctx.h, g))
+    torch.cuda.synchronize()
+    for o, (x, g, ref, ctx, stream) in zip(outs, runs):
+        with ctx as h:
+            _ok(pkv, h)
+            _attn_near(o[0], *ref)
+            assert all(torch.equal(o[0], y) for y in o[1:])

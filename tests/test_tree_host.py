@@ -77,6 +77,7 @@ def test_slot_map_refusals(pkv):
     assert call(pages_out=good["held"], left=good["count"]) == pkv.PKV_ERR_CUDA
     assert call(parents=None, mask=None, words=0) == pkv.PKV_ERR_CUDA       # a chain
     assert call(n=0, slots=None, positions=None) == pkv.PKV_ERR_CUDA
+    assert call(n=1 << 29) == pkv.PKV_ERR_UNSUPPORTED
     assert call(cap=0, free=None) == pkv.PKV_ERR_CUDA
 
 
@@ -109,6 +110,7 @@ def test_decode_attn_tree_refusals(pkv, fp8):
     call = lambda **kw: _call(pkv, "pkv_decode_attn_tree", good, TREE, **kw)   # noqa: E731
     assert call() == pkv.PKV_ERR_CUDA
     assert call(batch=0, q=None) == pkv.PKV_OK and call(n=0, q=None) == pkv.PKV_OK
+    assert call(n=1 << 29) == pkv.PKV_ERR_UNSUPPORTED
     bad = [dict(ctx=None), dict(batch=-1), dict(batch=9), dict(stride=0), dict(stride=65), dict(n=-1), dict(words=0),
            dict(q=_at(1, 8)), dict(out=_at(14, 8)), dict(cu=_at(9, 4)), dict(mask=_at(10, 2)), dict(out=good["q"]),
            dict(out=good["q"] + 16)]
@@ -162,6 +164,17 @@ def test_binding_checks_shapes(pkv):
                                  h(9, 32, 128), 0, 0, None, None)
     with pytest.raises(ValueError, match="device tensors"):
         pkv.pkv_tree_commit(ctx, 0, 0, None, None, i(2, 4), torch.zeros(2, dtype=torch.int32), i(2, 3), i(2), i(2))
+    class _Elsewhere(_OnDevice):
+        def get_device(self):
+            return 3
+
+    keep, pkv._cur_device = pkv._cur_device, lambda: 0
+    try:
+        with pytest.raises(ValueError, match="current device"):
+            pkv.pkv_tree_commit(ctx, 0, 0, None, None, torch.zeros(2, 4, dtype=torch.int32).as_subclass(_Elsewhere), i(2),
+                                i(2, 3), i(2), i(2))
+    finally:
+        pkv._cur_device = keep
     with pytest.raises(TypeError, match="path_lens"):
         pkv.pkv_tree_commit(ctx, 0, 0, None, None, i(2, 4), i(2), i(2, 3), i(2).long(), i(2))
 
