@@ -11,7 +11,7 @@
 // Mathematics: o = softmax(q K^T / sqrt(d)) V over the keys a row sees, all
 // cached keys and those drafted ones whose mask bit is set.  One pass with a
 // running reference m and sum l per row: S = Q K^T, P = 2^(s - m), l += P,
-// O += P V; m moves only when the row's maximum passes it by more than 2^8.
+// O += P V; m moves only when the row's maximum passes it by more than 2^24.
 //
 // Work item: a request, one of its kv heads and a block of up to 2 (128 / G)
 // of its new tokens; the G heads of the group times the tokens are the rows
@@ -28,7 +28,7 @@
 // in a fixed order.  Nothing waits for another CTA.
 //
 // Warps: 0 and 2 load Q, K and V (TMA), 1 issues the MMAs, 4 .. 11 softmax and
-// output, one thread per row; for E4M3 pools 12 .. 19 turn the codes into
+// output, one thread per row; for E4M3 pools 12 .. 15 turn the codes into
 // bf16 tiles (exact; the scales of a page and head go into the scores and the
 // weights in fp32).  P is rounded to bf16 for the matrix product, each weight off by at
 // most 2^-8 of itself; two terms of bf16 would cost half as much again on the
@@ -56,6 +56,11 @@ constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // times the mean.
 constexpr int kCostRowShift = 2, kCostKeyShift = 1, kCostItem = 9;
 constexpr int kCostRow = 1 << kCostRowShift, kCostKey = 1 << kCostKeyShift;
+// How far a row's maximum may pass its reference, in powers of two, before the
+// reference moves: the weights are bf16 and their sums fp32, of one exponent
+// range, so that nothing is lost below 2^24 (V up to 2^100); 2^8 cost E4M3
+// caches 4% in moves that changed nothing.
+constexpr float kSlack = 24.f;
 constexpr int kSnap = 2;                      // a cut this near to an item's ends moves there
 
 template <int D, bool FP8>
@@ -65,7 +70,7 @@ struct TreeGeo {
     static constexpr int NS = FP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
     static constexpr int NC = FP8 ? (D == 128 ? 4 : 6) : 0;          // tiles of codes
     static constexpr int STG = kTKeys * D;
-    static constexpr int THREADS = 128 + 256 + (FP8 ? 256 : 0);
+    static constexpr int THREADS = 128 + 256 + (FP8 ? 128 : 0);
     static constexpr int BYTES = (2 + NS) * SLOT + NC * STG + 1024;
 };
 
@@ -244,21 +249,32 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 // The scores of keys that the row does not see become -inf, whatever they
-// were (of tiles with drafted keys, or pages out of range, before the pass
-// below: masks in that pass would double its code for one tile in many).
-__device__ __forceinline__ void tile_mask(uint32_t scol, const uint32_t (&vis)[4])
+// were, before the pass below (masks in that pass would double its code for one
+// tile in many).  d0: the tile's first key counted in drafted tokens; seen(i):
+// word i of those the row sees; lost(k): keys 32 k .. of the tile in pages out of
+// range.  This and the rest of a segment's end run once for an item, from cold
+// instruction caches, where every line of code costs a fetch: short loops.
+template <class Seen, class Lost>
+__device__ __forceinline__ void tile_mask(uint32_t scol, int d0, Seen seen, Lost lost)
 {
+    uint32_t low = seen(d0 >> 5), see = 0u;
 #pragma unroll 1
-    for (int k = 0; k < 4; ++k) {
-        uint32_t x[4][8];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld8(scol + (uint32_t)(32 * k + 8 * c), x[c]);
-        const uint32_t see = k & 2 ? (k & 1 ? vis[3] : vis[2]) : (k & 1 ? vis[1] : vis[0]);
+    for (int c0 = 0; c0 < kTKeys; c0 += 16) {
+        if (c0 & 16) {
+            see >>= 16;
+        } else {
+            const uint32_t high = seen((d0 >> 5) + c0 / 32 + 1);
+            see = __funnelshift_r(low, high, d0 & 31) & ~lost(c0 / 32);
+            low = high;
+        }
+        uint32_t x[2][8];
+        tmem_ld8(scol + (uint32_t)c0, x[0]);
+        tmem_ld8(scol + (uint32_t)c0 + 8u, x[1]);
         tmem_wait_ld();
 #pragma unroll
-        for (int c = 0; c < 32; ++c) x[c >> 3][c & 7] = (see >> c) & 1u ? x[c >> 3][c & 7] : 0xFF800000u;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_st8(scol + (uint32_t)(32 * k + 8 * c), x[c]);
+        for (int c = 0; c < 16; ++c) x[c >> 3][c & 7] = (see >> c) & 1u ? x[c >> 3][c & 7] : 0xFF800000u;
+        tmem_st8(scol + (uint32_t)c0, x[0]);
+        tmem_st8(scol + (uint32_t)c0 + 8u, x[1]);
     }
     tmem_wait_st();
 }
@@ -286,7 +302,7 @@ __device__ __forceinline__ void tmem_scale16(uint32_t col, float alpha)
 // (unrolled, the code was over 64 KB, and fetching it made every warp of the SM
 // several times slower).  A chunk's maximum is taken
 // while its scores are in registers; the reference m, a whole number, moves
-// only when some row of the warp passes it by more than 2^8, and then what was
+// only when some row of the warp passes it by more than 2^24, and then what was
 // made with the old one (O of this stream, the tile's chunks of P, l) is
 // multiplied by a power of two, which is exact.  P = 2^(s - m) goes back as
 // bf16 over the S columns already read, keys 2i and 2i + 1 in column i.
@@ -325,7 +341,7 @@ __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool 
             mx = fmaxf(mx, FP8 ? y * fs[h] : y);
         }
         if (!FP8) mx *= f;
-        if (__any_sync(0xffffffffu, mx > m + 8.f)) {
+        if (__any_sync(0xffffffffu, mx > m + kSlack)) {
             const float mn = fmaxf(m, ceilf(mx)), alpha = m == mn ? 1.f : ex2(m - mn);
             if (!first) {          // S of this tile was issued after the last P V of the stream: O is settled
 #pragma unroll 1
@@ -496,19 +512,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
     }
     Segment s;
 
-    // E4M3: 640 threads of 96 registers at the start; the softmax takes what the
-    // others do not need (144 x 256 + 64 x 384 = 96 x 640)
     if (warp < 4) {
-        if (FP8) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
         if (warp == 0 || warp == 2) {
-            // ---- loads, in the order of their use, by warps 0 and 2 (a box takes
+            // ---- loads: warp 0 those of Q and K, warp 2 those of V (a box takes
             // about 100 cycles to issue: one warp alone was what bounded pages of
-            // 16 tokens).  bf16: warp 0 those of Q and K, warp 2 those of V.  E4M3:
-            // each issues every other box of every load (183 us; by K and V 198).
-            // A warp waits for its own places only.  A parity tells two phases
-            // apart, so that needs its last place within a ring before the next
-            // one: they are at most 3 apart.
-            const int half = warp >> 1;
+            // 16 tokens).  A warp waits for its own places of the ring only.  A
+            // parity tells two phases apart, so that needs its last place within
+            // a ring before the next one: they are at most 3 apart.
+            const bool is_k = warp == 0;
             constexpr int N = FP8 ? NCX : NS;
             constexpr int ROWB = FP8 ? D : 2 * D;                // bytes of a row in the pool
             const uint32_t lfull = FP8 ? cfull : full, lempty = FP8 ? cempty : empty, dst0 = FP8 ? stage : ring;
@@ -542,14 +553,10 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     __syncwarp();
                     ++count;
                 };
-                const int lead = lead_of(s);
-                int ik = 0, iv = 0, kpage = page_of(0), vpage = kpage;
-                while (ok) {
-                    const bool is_k = FP8 ? ik < s.n && ik < iv + lead : half == 0;
-                    if ((is_k ? ik : iv) >= s.n) break;
-                    const int seq = rb + (is_k ? k_seq(s, ik) : v_seq(s, iv)), cur = is_k ? kpage : vpage;
-                    if (is_k) kpage = page_of(++ik);
-                    else vpage = page_of(++iv);
+                int page = page_of(0);
+                for (int i = 0; ok && i < s.n; ++i) {
+                    const int seq = rb + (is_k ? k_seq(s, i) : v_seq(s, i)), cur = page;
+                    page = page_of(i + 1);
                     const int j = seq % N;
                     if (seq >= N) wait(lempty + 8u * j, seq / N - 1);
                     if (!ok) break;
@@ -559,7 +566,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     }
                     const int np = __popc(__ballot_sync(0xffffffffu, cur != -2));
                     const int y = cur < 0 ? -p.P : (cur * p.Hkv + s.kvh) * p.P;
-                    if ((!FP8 || half == 0) && elect_one()) {
+                    if (elect_one()) {
                         s_issued[j] = seq / N + 1;
                         mbar_arrive_expect_tx(lfull + 8u * j, (uint32_t)(np * p.P * ROWB));
                     }
@@ -567,14 +574,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     uint32_t dst = dst0 + (uint32_t)(j * LSLOT);
                     for (int k = 0; k < np; ++k) {
                         const int yk = __shfl_sync(0xffffffffu, y, k);
-                        if ((!FP8 || (k & 1) == half) && elect_one()) {
+                        if (elect_one()) {
 #pragma unroll
                             for (int kb = 0; kb < LB; ++kb) tma_load_2d(dst + (uint32_t)(kb * kTBlk), map, 64 * kb, yk, lfull + 8u * j);
                         }
                         dst += (uint32_t)(p.P * (FP8 ? D : 128));
                     }
                     __syncwarp();
-                    if (half == 0 && ik + iv == 1) {         // the first tile is under way: now Q, once it is free
+                    if (is_k && i == 0) {                        // the first tile is under way: now Q, once it is free
                         if (s.row_mode) {
                             load_q(0, qc0, s.row0);
                             load_q(1, qc1, s.row0 + p.tb);
@@ -683,7 +690,7 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             __syncwarp();
         }
     } else if (warp < 12) {
-        if (FP8) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
+        
         // ---- softmax and output: row r of stream st
         const int st = (warp - 4) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const int rtok = (r * p.g_inv) >> 16, g = r - rtok * p.G;
@@ -744,22 +751,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const bool tail = key0 + kTKeys > s.L;
                 if (ok && act) {
                     if (tail || bad) {
-                        uint32_t vis[4];
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int d0 = key0 - s.L + 32 * w;
-                            vis[w] = __funnelshift_r(seen(d0 >> 5), seen((d0 >> 5) + 1), d0 & 31);
-                        }
-                        for (int k = 0; bad && k < (kTKeys >> shift); ++k) {
-                            const int at = (key0 >> shift) + k;
-                            if (at * p.P >= n_keys || (unsigned)__ldg(&bt[at]) < (unsigned)p.num_pages) continue;
-#pragma unroll
-                            for (int w = 0; w < 4; ++w) {          // the page's keys: 16 or 32 bits of a word, or two words
-                                const int c = (k << shift) - 32 * w;
-                                if (c > -p.P && c < 32) vis[w] &= ~((shift == 4 ? 0xFFFFu : 0xFFFFFFFFu) << max(c, 0));
+                        auto lost = [&](int k) {
+                            uint32_t gone = 0u;
+#pragma unroll 1
+                            for (int c = 0; bad && c < 32; c += 16) {
+                                const int at = (key0 + 32 * k + c) >> shift;
+                                if (at * p.P < n_keys && (unsigned)__ldg(&bt[at]) >= (unsigned)p.num_pages) gone |= 0xFFFFu << c;
                             }
-                        }
-                        tile_mask(scol, vis);
+                            return gone;
+                        };
+                        tile_mask(scol, key0 - s.L, seen, lost);
                     }
                     tile_softmax<D, FP8>(scol, lanes + kTOcol + (uint32_t)(st * 128), u < 2, p.scale_log2, scales, shift, m, l);
                 }
@@ -774,34 +775,23 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     if (ok) {
                         bool wrote = false;
                         const int pieces = (min(kTKeys, (z0 + 15) & ~15) - d0) * KB * 8;      // up to the last step of P V
-                        for (int x0 = 32 * quarter + lane; x0 < pieces; x0 += 512) {
-                            uint4 v[4];
-                            uint32_t addr[4];
+#pragma unroll 1
+                        for (int x = 32 * quarter + lane; x < pieces; x += 128) {
+                            const int row = d0 + x / (KB * 8), rem = x % (KB * 8);
+                            const uint32_t addr = va + (uint32_t)((rem >> 3) * kTBlk + row * 128 + (rem & 7) * 16);
+                            const uint4 v = lds128(addr);
+                            uint32_t w[4] = {v.x, v.y, v.z, v.w}, odd[4], any = 0u;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int x = x0 + 128 * k, row = d0 + x / (KB * 8), rem = x % (KB * 8);
-                                addr[k] = va + (uint32_t)((rem >> 3) * kTBlk + row * 128 + (rem & 7) * 16);
-                                if (x < pieces) v[k] = lds128(addr[k]);
+                            for (int k = 0; k < 4; ++k) {          // bit 15 of a half: its exponent is all ones
+                                odd[k] = ((w[k] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+                                any |= odd[k];
                             }
+                            if (row < z0 && !any) continue;
+                            if (row < z0) s_odd = 1;
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int x = x0 + 128 * k, row = d0 + x / (KB * 8);
-                                if (x >= pieces) break;
-                                uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
-                                bool change = row >= z0;
-#pragma unroll
-                                for (int i2 = 0; i2 < 4; ++i2) {
-                                    const bool lo = (w[i2] & 0x7F80u) == 0x7F80u, hi = (w[i2] & 0x7F800000u) == 0x7F800000u;
-                                    if (row >= z0) w[i2] = 0u;
-                                    else if (lo || hi) {
-                                        w[i2] &= (lo ? 0xFFFF0000u : ~0u) & (hi ? 0xFFFFu : ~0u);
-                                        change = true;
-                                        s_odd = 1;
-                                    }
-                                }
-                                if (change) sts128(addr[k], make_uint4(w[0], w[1], w[2], w[3]));
-                                wrote = wrote || change;
-                            }
+                            for (int k = 0; k < 4; ++k) w[k] = row < z0 ? w[k] & ~((odd[k] >> 15) * 0xFFFFu) : 0u;
+                            sts128(addr, make_uint4(w[0], w[1], w[2], w[3]));
+                            wrote = true;
                         }
                         if (wrote) fence_proxy_async_smem();
                     }
@@ -847,51 +837,56 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 __nv_bfloat16* const orow = p.out + (trow * p.Hq + (size_t)s.kvh * p.G + g) * D;
                 if (valid && s.place && (s.row_mode || st == 0)) p.part_ml[slot_row] = make_float2(m, l);
 #pragma unroll 1
-                for (int c0 = col0; c0 < col0 + cols; c0 += 32) {
-                    uint32_t x0[32];
-                    float o[32];
-                    tmem_ld32(lanes + kTOcol + (uint32_t)((s.row_mode ? st * 128 : 0) + c0), x0);
+                for (int c0 = col0; c0 < col0 + cols; c0 += 16) {
+                    uint32_t x[2][8];
+                    float o[16];
+                    const uint32_t oc = lanes + kTOcol + (uint32_t)((s.row_mode ? st * 128 : 0) + c0);
+                    tmem_ld8(oc, x[0]);
+                    tmem_ld8(oc + 8u, x[1]);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) o[c] = s.row_mode ? __uint_as_float(x0[c]) : a0 * __uint_as_float(x0[c]);
+                    for (int c = 0; c < 16; ++c) o[c] = __uint_as_float(x[c >> 3][c & 7]) * (s.row_mode ? 1.f : a0);
                     if (both) {
-                        tmem_ld32(lanes + kTOcol + 128u + (uint32_t)c0, x0);
+                        tmem_ld8(oc + 128u, x[0]);
+                        tmem_ld8(oc + 136u, x[1]);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = fmaf(a1, __uint_as_float(x0[c]), o[c]);
-                    }
-                    if (odd && valid) {      // numbers that are not finite in V of the drafted tokens this row sees
-                        const int j1 = min(s.T, (s.t0 + s.n) * kTKeys - s.L);
-                        for (int j = max(0, s.t0 * kTKeys - s.L); j < j1; ++j) {
-                            if (!((seen(j >> 5) >> (j & 31)) & 1u)) continue;
-                            const int page = bt[(s.L + j) >> shift];
-                            if ((unsigned)page >= (unsigned)p.num_pages) continue;
-                            const size_t at = (((size_t)page * p.Hkv + s.kvh) * p.P + ((s.L + j) & (p.P - 1))) * D + c0;
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                float v;
-                                if (FP8) {
-                                    const __nv_fp8_storage_t code = reinterpret_cast<const uint8_t*>(p.v_pool)[at + c];
-                                    v = __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
-                                } else {
-                                    v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v_pool)[at + c]);
-                                }
-                                if (!isfinite(v)) o[c] += v;
-                            }
-                        }
+                        for (int c = 0; c < 16; ++c) o[c] = fmaf(a1, __uint_as_float(x[c >> 3][c & 7]), o[c]);
                     }
                     if (!valid) continue;
                     if (s.place == 0) {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 8)
+                        for (int c = 0; c < 16; c += 8)
                             *reinterpret_cast<uint4*>(orow + c0 + c) =
                                 make_uint4(pack_bf16(o[c] * inv, o[c + 1] * inv), pack_bf16(o[c + 2] * inv, o[c + 3] * inv),
                                            pack_bf16(o[c + 4] * inv, o[c + 5] * inv), pack_bf16(o[c + 6] * inv, o[c + 7] * inv));
                     } else {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4)
+                        for (int c = 0; c < 16; c += 4)
                             *reinterpret_cast<float4*>(p.part_o + slot_row * D + c0 + c) =
                                 make_float4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    }
+                }
+                // numbers that are not finite in V of the drafted tokens this row sees
+                const int j1 = min(s.T, (s.t0 + s.n) * kTKeys - s.L);
+#pragma unroll 1
+                for (int j = max(0, s.t0 * kTKeys - s.L); odd && valid && j < j1; ++j) {
+                    if (!((seen(j >> 5) >> (j & 31)) & 1u)) continue;
+                    const int page = bt[(s.L + j) >> shift];
+                    if ((unsigned)page >= (unsigned)p.num_pages) continue;
+                    const size_t at = (((size_t)page * p.Hkv + s.kvh) * p.P + ((s.L + j) & (p.P - 1))) * D;
+#pragma unroll 1
+                    for (int c = col0; c < col0 + cols; ++c) {
+                        float v;
+                        if (FP8) {
+                            const __nv_fp8_storage_t code = reinterpret_cast<const uint8_t*>(p.v_pool)[at + c];
+                            v = __half2float(__half(__nv_cvt_fp8_to_halfraw(code, __NV_E4M3)));
+                        } else {
+                            v = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.v_pool)[at + c]);
+                        }
+                        if (isfinite(v)) continue;
+                        if (s.place == 0) orow[c] = __float2bfloat16_rn(__bfloat162float(orow[c]) + v);
+                        else p.part_o[slot_row * D + c] += v;
                     }
                 }
             }
@@ -901,15 +896,16 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
         }
         if (!ok) s_fail = 1;
     } else if (FP8) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-        // ---- codes to bf16: warps 12 .. 15 the even loads, 16 .. 19 the odd
-        // ones; lane l of a warp takes row 8 k + l % 8, 16 codes l / 8 + 4 j
+        // ---- codes to bf16: lane l of a warp takes rows 8 k + l % 8, 16 codes l / 8
+        // + 4 j.  Eight warps, with the registers of the others, were slower (177
+        // us against 169): they take issue slots and instruction fetches from the
+        // softmax, whose chain the tiles wait for
         const int w = warp & 3;
         int rb = 0;
         bool ok = true;
         while (ok && walk.next(p, s)) {
             const int end = rb + 2 * s.n;
-            for (int q = rb + ((rb ^ ((warp - 12) >> 2)) & 1); q < end; q += 2) {
+            for (int q = rb; q < end; ++q) {
                 const int c = q % NCX, slot = q % NS;
                 ok = __all_sync(0xffffffffu, wait_bar(cfull + 8u * c, (uint32_t)((q / NCX) & 1))) != 0;
                 if (ok && q >= NS) ok = __all_sync(0xffffffffu, wait_bar(empty + 8u * slot, (uint32_t)((q / NS - 1) & 1))) != 0;
