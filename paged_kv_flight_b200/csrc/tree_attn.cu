@@ -30,9 +30,18 @@
 // Warps: 0 and 2 load Q, K and V (TMA), 1 issues the MMAs, 4 .. 11 softmax and
 // output, one thread per row; for E4M3 pools 12 .. 15 turn the codes into
 // bf16 tiles (exact; the scales of a page and head go into the scores and the
-// weights in fp32).  P is rounded to bf16 for the matrix product, each weight off by at
-// most 2^-8 of itself; two terms of bf16 would cost half as much again on the
-// tensor pipe, which bounds the large trees.
+// weights in fp32).  P is rounded to bf16 for the matrix product, each weight off
+// by at most 2^-8 of itself, as the output is; a second bf16 term for what is left
+// made the large trees 10% slower.
+//
+// What bounds it, and what it measured (B200, us a call): long caches, memory (8
+// requests of 32k to 128k tokens, 8 new ones each, 2.28 GB: 361, 98% of the
+// measured copy; 64 requests of 128 to 4096, 9 to 16 new ones, 555 MB: 113, 76%);
+// large trees, the chain of a tile, S, softmax, P V and the handovers between
+// them, of which tensor memory holds two at d = 128 (48 requests, 33 to 64 new
+// tokens of 64 heads: 164, where the products alone take 52); E4M3 caches, the
+// same beside the conversion (64 requests, 391 MB: 159); a few short requests,
+// latency (4 requests: 11.8).
 #include "tree_params.h"
 #include "pkv_device.cuh"
 #include "umma.cuh"
@@ -51,9 +60,10 @@ constexpr int kMaxSlots = 8;
 constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // Cost of a tile for the cut, and of an item besides its tiles (Q, the masked
 // tile, the merge of the streams, the output).  Fitted over the CTAs of three
-// workloads: 4758 cycles a tile in row mode, 2450 to 2790 in key mode, 10.6 to
-// 14.2 thousand an item.  Cut by tiles alone, the slowest CTA took 1.5 to 2
-// times the mean.
+// workloads: 3900 cycles a tile in row mode, 1950 in key mode, 8.7 to 12 thousand
+// an item.  Cut by tiles alone, the slowest CTA took 1.5 to 2 times the mean (297
+// us against 184 for large trees); with 7 or 12 for the item they took 3 and 2%
+// longer.
 constexpr int kCostRowShift = 2, kCostKeyShift = 1, kCostItem = 9;
 constexpr int kCostRow = 1 << kCostRowShift, kCostKey = 1 << kCostKeyShift;
 // How far a row's maximum may pass its reference, in powers of two, before the
