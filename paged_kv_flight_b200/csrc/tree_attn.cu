@@ -32,7 +32,7 @@
 // bf16 tiles (exact; the scales of a page and head go into the scores and the
 // weights in fp32).  P is rounded to bf16 for the matrix product, each weight off
 // by at most 2^-8 of itself, as the output is; a second bf16 term for what is left
-// made the large trees 10% slower.
+// would be half as many MMAs again.
 //
 // What bounds it, and what it measured (B200, us a call): long caches, memory (8
 // requests of 32k to 128k tokens, 8 new ones each, 2.28 GB: 361, 98% of the
@@ -978,14 +978,14 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
 
 // ---- merge of the items that the cut went through -----------------------------------
 
-constexpr int kCombineThreads = 256;
-constexpr int kCombineGroups = 4;       // blocks per cut, each a share of the item's rows: one wave of blocks in all
+constexpr int kCombineThreads = 128;
+constexpr int kCombineGroups = 8;       // blocks per cut, each a share of the item's rows
 constexpr int kRowLanes = 16;           // lanes of a row
 
 // Block (i, y): if cut i + 1 is the first inside its item, the parts of that
 // item: the last segment of run i, then the first segments of the runs behind.
-// Bound by a chain of dependent loads (places, lengths, parts): 16 lanes a row
-// keep two rows of 32 bytes a lane in flight in every warp.
+// Bound by a chain of dependent loads (places, lengths, parts): 16 lanes take a
+// row, and what they need of four parts is under way together.
 template <int D>
 __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const TreeAttnParams p, int W)
 {
@@ -1019,23 +1019,35 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
         const int half = ntok > p.tb && q >= p.tb * p.G ? 1 : 0, in_half = q - half * p.tb * p.G;
         const int tok_in = (in_half * p.g_inv) >> 16, g = in_half - tok_in * p.G, tok = half * p.tb + tok_in;
         const size_t row = (size_t)(half * kTRows + in_half);
-        float m = -INFINITY;
-        for (int c = 0; c < n; ++c) m = fmaxf(m, p.part_ml[(size_t)s_slot[c] * 2 * kTRows + row].x);
-        float l = 0.f, acc[E];
+        float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = 0.f;
-#pragma unroll 2
-        for (int c = 0; c < n; ++c) {
-            const size_t at = (size_t)s_slot[c] * 2 * kTRows + row;
-            const float2 ml = p.part_ml[at];
-            const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-            float v[E];
+#pragma unroll 1
+        for (int c0 = 0; c0 < n; c0 += 4) {
+            float2 ml[4];
+            float4 v[4][E / 4];
 #pragma unroll
-            for (int e = 0; e < E; e += 4)
-                *reinterpret_cast<float4*>(&v[e]) = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * E + e);
-            l = fmaf(f, ml.y, l);
+            for (int k = 0; k < 4; ++k) {
+                const size_t at = (size_t)s_slot[min(c0 + k, n - 1)] * 2 * kTRows + row;
+                ml[k] = p.part_ml[at];
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = fmaf(f, v[e], acc[e]);
+                for (int e = 0; e < E / 4; ++e) v[k][e] = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * E + 4 * e);
+                if (c0 + k >= n) ml[k].x = -INFINITY;
+            }
+            const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
+            const float old = m == -INFINITY ? 0.f : ex2(m - mn);
+            l *= old;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] *= old;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - mn);
+                if (f == 0.f) continue;                    // nothing of it, whatever it holds
+                l = fmaf(f, ml[k].y, l);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = fmaf(f, reinterpret_cast<const float*>(v[k])[e], acc[e]);
+            }
+            m = mn;
         }
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
         uint32_t w[E / 2];
