@@ -1,4 +1,5 @@
-"""Build libpkv.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc.
+"""Build libpkv.so (the C-ABI CUDA library) in-tree for sm_100a with nvcc, and
+_marshal.so (the Python binding's argument checks) with the host compiler.
 
     python -m paged_kv_flight_b200.build [--force] [--ptxas-v]
 """
@@ -6,11 +7,14 @@ import glob
 import os
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libpkv.so")
+MARSHAL_SRC = os.path.join(CSRC, "marshal.cc")
+MARSHAL = os.path.join(HERE, "_marshal.so")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -33,6 +37,29 @@ def needs_build() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_marshal(force: bool = False, verbose: bool = False) -> str:
+    """The binding's extension module, against the installed torch's headers.
+    pkv.py does its work in Python where it is missing, so that a host without
+    a C++ compiler or those headers still has the library."""
+    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC):
+        return MARSHAL
+    import torch
+
+    base = os.path.dirname(torch.__file__)
+    inc = os.path.join(base, "include")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-o", MARSHAL,
+           MARSHAL_SRC, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    if verbose:
+        print(" ".join(cmd))
+    try:
+        subprocess.run(cmd, check=True)
+    except (OSError, subprocess.CalledProcessError) as e:
+        print(f"_marshal.so not built ({e}): the binding's checks stay in Python", file=sys.stderr)
+    return MARSHAL
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if force or needs_build() or extra:
         nvcc = os.environ.get("NVCC", "nvcc")
@@ -40,6 +67,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         if verbose:
             print(" ".join(cmd))
         subprocess.run(cmd, check=True)
+    build_marshal(force, verbose)
     return LIB
 
 

@@ -27,7 +27,7 @@
 //
 // Measured (B200): 256 requests, 4.7 thousand tokens in trees of up to 32, 8.0 us
 // on the device (9.0 with the walks in L2 and a grid of small CTAs); 4 requests
-// of one token, 5.7 us (7.0); in a loop of calls the host's 10 us bound both.
+// of one token, 5.7 us (7.0).
 #include "tree_params.h"
 
 namespace pkv {

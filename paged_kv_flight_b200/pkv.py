@@ -123,7 +123,7 @@ lib.pkv_decode_step.restype = C.c_int
 _I = C.c_int
 lib.pkv_slot_map.argtypes = [_V, _V, _V, _V, _I, _V, _I, _V, _V, _V, _I, _V, _V, _I, _I, _V, _V, _V, _V, _V]
 lib.pkv_slot_map.restype = _I
-lib.pkv_rope_append_axes.argtypes = [_V, _V, _V, _V, _I, _V, _I, C.POINTER(_I), _I, _V, _V, _V, _V, _V, _V, _V]
+lib.pkv_rope_append_axes.argtypes = [_V, _V, _V, _V, _I, _V, _I, _V, _I, _V, _V, _V, _V, _V, _V, _V]
 lib.pkv_rope_append_axes.restype = _I
 lib.pkv_decode_attn_tree.argtypes = [_V, _V, _V, _V, _V, _V, _V, _I, _V, _V, _V, _I, _I, _I, _V, _V]
 lib.pkv_decode_attn_tree.restype = _I
@@ -501,33 +501,56 @@ def _rows(x, shape, name):
                          f"got {tuple(x.shape)}")
 
 
-_Tensor, _i32, _bf16 = torch.Tensor, torch.int32, torch.bfloat16
+_Tensor = torch.Tensor
+try:
+    from . import _marshal
+    _pointer, _call = _marshal.pointer, _marshal.call
+except ImportError:                      # not built: the same checks, in Python alone
+    def _pointer(*_):
+        return None
+
+    def _call(function, *args):
+        return function(*args)
+else:
+    del _marshal
+
+
+def _entry(name):
+    """The library function as _call takes it."""
+    f = getattr(lib, name)
+    return f if _call.__module__ == __name__ else C.cast(f, _V).value
 
 
 def _vec(x, n, name):
-    """Device pointer of an int32 vector of n entries (_rows, then _ptr; the
-    calls of a small step are bound by the host, so what is right takes one
-    line)."""
-    if type(x) is _Tensor and x.dtype is _i32 and x.is_cuda and x.dim() == 1 and x.numel() == n and x.is_contiguous():
-        return x.data_ptr()
+    """Device pointer of an int32 vector of n entries; raises what is wrong
+    with it.  (The calls below ask _pointer first, which is quick and says
+    nothing of the reason: those of a small step are bound by the host.)"""
     _rows(x, (n,), name)
     return _ptr(x, _I32, name)
 
 
 def _mat(x, shape, name):
     """The same of an int32 tensor of the given shape."""
-    if type(x) is _Tensor and x.dtype is _i32 and x.is_cuda and x.shape == shape and x.is_contiguous():
-        return x.data_ptr()
     _rows(x, shape, name)
     return _ptr(x, _I32, name)
 
 
 def _act(x, shape, name):
     """The same of a bf16 tensor of the given shape."""
-    if type(x) is _Tensor and x.dtype is _bf16 and x.is_cuda and x.shape == shape and x.is_contiguous():
-        return x.data_ptr()
     _rows(x, shape, name)
     return _ptr(x, _ACT, name)
+
+
+_K_I32, _K_BF16, _K_POOL, _K_F32 = range(4)       # element kinds of _pointer
+_slot_map, _rope_axes, _attn_tree, _commit = (_entry(f) for f in EXPORTS[-4:])
+
+
+def _pools(k_pool, v_pool, k_scale, v_scale):
+    """_kv, quicker."""
+    return (_pointer(k_pool, _K_POOL) or _ptr(k_pool, _POOL, "k_pool"),
+            _pointer(v_pool, _K_POOL) or _ptr(v_pool, _POOL, "v_pool"),
+            None if k_scale is None else _pointer(k_scale, _K_F32) or _ptr(k_scale, _F32, "k_scale"),
+            None if v_scale is None else _pointer(v_scale, _K_F32) or _ptr(v_scale, _F32, "v_scale"))
 
 
 def _sizes(x, n, name):
@@ -558,13 +581,20 @@ def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, 
     cap, = _sizes(free_pages, 1, "free_pages")
     words = 0 if tree_mask is None else _sizes(tree_mask, 2, "tree_mask")[1]
     _here(block_tables, "block_tables")
-    st = lib.pkv_slot_map(ctx, _vec(seq_lens, B, "seq_lens"), _vec(new_lens, B, "new_lens"),
-                          None if parents is None else _vec(parents, n, "parents"), B,
-                          _mat(block_tables, (B, stride), "block_tables"), stride, _vec(pages_held, B, "pages_held"),
-                          _vec(pages_out, B, "pages_out"), _vec(free_pages, cap, "free_pages"), cap,
-                          _vec(free_count, 1, "free_count"), _vec(free_left, 1, "free_left"), n, words,
-                          _vec(cu_q, B + 1, "cu_q"), _vec(slots, n, "slots"), _vec(positions, n, "positions"),
-                          None if tree_mask is None else _mat(tree_mask, (n, words), "tree_mask"), _stream(stream))
+    p = _pointer
+    st = _call(_slot_map, ctx, p(seq_lens, 0, B) or _vec(seq_lens, B, "seq_lens"),
+               p(new_lens, 0, B) or _vec(new_lens, B, "new_lens"),
+               None if parents is None else p(parents, 0, n) or _vec(parents, n, "parents"), B,
+               p(block_tables, 0, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
+               p(pages_held, 0, B) or _vec(pages_held, B, "pages_held"),
+               p(pages_out, 0, B) or _vec(pages_out, B, "pages_out"),
+               p(free_pages, 0, cap) or _vec(free_pages, cap, "free_pages"), cap,
+               p(free_count, 0, 1) or _vec(free_count, 1, "free_count"),
+               p(free_left, 0, 1) or _vec(free_left, 1, "free_left"), n, words,
+               p(cu_q, 0, B + 1) or _vec(cu_q, B + 1, "cu_q"), p(slots, 0, n) or _vec(slots, n, "slots"),
+               p(positions, 0, n) or _vec(positions, n, "positions"),
+               None if tree_mask is None else p(tree_mask, 0, n, words) or _mat(tree_mask, (n, words), "tree_mask"),
+               _stream(stream))
     return _done(st, "pkv_slot_map", check)
 
 
@@ -579,11 +609,15 @@ def pkv_rope_append_axes(ctx, q, k_new, v_new, positions, sections, slots, q_out
     if k_shape[0] != n or k_shape[2] != q_shape[2]:
         raise ValueError(f"k_new: shape {tuple(k_shape)} next to q of {tuple(q_shape)}")
     _here(q, "q")
-    st = lib.pkv_rope_append_axes(ctx, _act(q, q_shape, "q"), _act(k_new, k_shape, "k_new"),
-                                  _act(v_new, k_shape, "v_new"), n, _mat(positions, (axes, n), "positions"), axes,
-                                  (_I * axes)(*sections), 1 if interleaved else 0, _vec(slots, n, "slots"),
-                                  _act(q_out, q_shape, "q_out"), *_kv(k_pool, v_pool, k_scale, v_scale),
-                                  _stream(stream))
+    p, h, hk, d = _pointer, q_shape[1], k_shape[1], q_shape[2]
+    sec = (_I * axes)(*sections)
+    st = _call(_rope_axes, ctx, p(q, 1, n, h, d) or _act(q, q_shape, "q"),
+               p(k_new, 1, n, hk, d) or _act(k_new, k_shape, "k_new"),
+               p(v_new, 1, n, hk, d) or _act(v_new, k_shape, "v_new"), n,
+               p(positions, 0, axes, n) or _mat(positions, (axes, n), "positions"), axes, C.addressof(sec),
+               1 if interleaved else 0, p(slots, 0, n) or _vec(slots, n, "slots"),
+               p(q_out, 1, n, h, d) or _act(q_out, q_shape, "q_out"), *_pools(k_pool, v_pool, k_scale, v_scale),
+               _stream(stream))
     return _done(st, "pkv_rope_append_axes", check)
 
 
@@ -597,11 +631,12 @@ def pkv_decode_attn_tree(ctx, q, k_pool, v_pool, k_scale, v_scale, block_tables,
     words = _sizes(tree_mask, 2, "tree_mask")[1]
     n = q_shape[0]
     _here(q, "q")
-    st = lib.pkv_decode_attn_tree(ctx, _act(q, q_shape, "q"), *_kv(k_pool, v_pool, k_scale, v_scale),
-                                  _mat(block_tables, (B, stride), "block_tables"), stride,
-                                  _vec(seq_lens, B, "seq_lens"), _vec(cu_q, B + 1, "cu_q"),
-                                  _mat(tree_mask, (n, words), "tree_mask"), words, B, n, _act(out, q_shape, "out"),
-                                  _stream(stream))
+    p, h, d = _pointer, q_shape[1], q_shape[2]
+    st = _call(_attn_tree, ctx, p(q, 1, n, h, d) or _act(q, q_shape, "q"), *_pools(k_pool, v_pool, k_scale, v_scale),
+               p(block_tables, 0, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
+               p(seq_lens, 0, B) or _vec(seq_lens, B, "seq_lens"), p(cu_q, 0, B + 1) or _vec(cu_q, B + 1, "cu_q"),
+               p(tree_mask, 0, n, words) or _mat(tree_mask, (n, words), "tree_mask"), words, B, n,
+               p(out, 1, n, h, d) or _act(out, q_shape, "out"), _stream(stream))
     return _done(st, "pkv_decode_attn_tree", check)
 
 
@@ -612,8 +647,11 @@ def pkv_tree_commit(ctx, k_pool, v_pool, k_scale, v_scale, block_tables, seq_len
     B, stride = _sizes(block_tables, 2, "block_tables")
     depth = _sizes(path, 2, "path")[1]
     _here(block_tables, "block_tables")
-    st = lib.pkv_tree_commit(ctx, *_kv(k_pool, v_pool, k_scale, v_scale),
-                             _mat(block_tables, (B, stride), "block_tables"), stride, _vec(seq_lens, B, "seq_lens"),
-                             _mat(path, (B, depth), "path"), depth, _vec(path_lens, B, "path_lens"), B,
-                             _vec(lens_out, B, "lens_out"), _stream(stream))
+    p = _pointer
+    st = _call(_commit, ctx, *_pools(k_pool, v_pool, k_scale, v_scale),
+               p(block_tables, 0, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
+               p(seq_lens, 0, B) or _vec(seq_lens, B, "seq_lens"),
+               p(path, 0, B, depth) or _mat(path, (B, depth), "path"), depth,
+               p(path_lens, 0, B) or _vec(path_lens, B, "path_lens"), B,
+               p(lens_out, 0, B) or _vec(lens_out, B, "lens_out"), _stream(stream))
     return _done(st, "pkv_tree_commit", check)

@@ -876,3 +876,17 @@ def test_two_contexts_on_two_streams(pkv):
             _ok(pkv, h)
             _attn_near(o[0], *ref)
             assert all(torch.equal(o[0], y) for y in o[1:])
+
+
+def test_marshal_pointers(pkv):
+    """The extension module takes what the checks in Python take, no more."""
+    m = pytest.importorskip("paged_kv_flight_b200._marshal")
+    kinds = {0: torch.int32, 1: torch.bfloat16, 2: torch.float8_e4m3fn, 3: torch.float32}
+    for k, dt in kinds.items():
+        x = torch.zeros(4, 6, device=DEV).to(dt)
+        assert m.pointer(x, k, 4, 6) == m.pointer(x, k) == m.pointer(x, k, -1, 6) == x.data_ptr()
+        for bad in (m.pointer(x, k, 6, 4), m.pointer(x, k, 24), m.pointer(x, k, 4, 6, 1), m.pointer(x.t(), k, 6, 4),
+                    m.pointer(x[:, ::2], k, 4, 3), m.pointer(x.cpu(), k, 4, 6), m.pointer(x.half(), k, 4, 6)):
+            assert bad is None
+        assert m.pointer(x[2], k, 6) == x.data_ptr() + 12 * x.element_size()
+    assert m.pointer(torch.zeros(2, device=DEV, dtype=torch.uint8), 2) and m.pointer(torch.zeros(2, device=DEV), 2) is None

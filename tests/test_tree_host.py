@@ -197,3 +197,60 @@ def test_plain_forms_agree():
     k = rng.standard_normal((1, 1, 16, 64))
     o, _ = _tree.attention(x[:1], k, k, [0], [0, 1], np.zeros((1, 1), np.int32), np.ones((1, 1), np.int32), 16, 2)
     assert np.allclose(o[0, 1], k[0, 0, 0])
+
+
+def test_marshal_module(pkv):
+    """The binding's extension module: what it takes for a device tensor, and
+    that a call's arguments arrive in order, None as NULL, whatever their sign."""
+    m = pytest.importorskip("paged_kv_flight_b200._marshal")
+    x = torch.zeros(3, dtype=torch.int32)
+    assert m.pointer(x, 0, 3) is None and m.pointer(7, 0) is None and m.pointer(None, 2) is None     # not on a device
+    with pytest.raises(TypeError):
+        m.pointer(x)
+    got = []
+    kind = C.CFUNCTYPE(C.c_int, *[C.c_int64] * 20)
+    back = kind(lambda *a: got.append(a) or 5)
+    address = C.cast(back, C.c_void_p).value
+    args = [1, None, -1, 2 ** 63, 2 ** 40 + 3] + list(range(5, 20))
+    assert m.call(address, *args) == 5
+    assert got[0] == tuple([1, 0, -1, -2 ** 63, 2 ** 40 + 3] + list(range(5, 20)))
+    for bad in ((address, "x"), (address, 1.5), (), (address, *range(21))):
+        with pytest.raises(TypeError):
+            m.call(*bad)
+    assert len(got) == 1
+
+
+def test_binding_without_the_marshal_module():
+    """The same refusals and calls where the extension module is not built."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+import sys
+sys.modules['paged_kv_flight_b200._marshal'] = None
+import torch
+from paged_kv_flight_b200 import pkv
+from tests.test_tree_host import _ctx
+class T(torch.Tensor):
+    is_cuda = True
+i = lambda *s: torch.zeros(*s, dtype=torch.int32).as_subclass(T)
+h = lambda *s: torch.zeros(*s, dtype=torch.bfloat16).as_subclass(T)
+ctx = _ctx(pkv)
+def status(f, *a, **k):
+    try:
+        return f(*a, check=False, stream=0, **k)
+    except Exception as e:
+        return type(e).__name__
+want = pkv.PKV_ERR_CUDA, 'ValueError'
+got = (status(pkv.pkv_slot_map, ctx, i(2), i(2), i(2, 4), i(2), i(9), i(1), i(3), i(5), i(5), i(2), i(1)),
+       status(pkv.pkv_slot_map, ctx, i(2), i(3), i(2, 4), i(2), i(9), i(1), i(3), i(5), i(5), i(2), i(1)))
+assert got == want, got
+pool = 1 << 33
+got = (status(pkv.pkv_rope_append_axes, ctx, h(2, 32, 128), h(2, 8, 128), h(2, 8, 128), i(1, 2), [64], i(2), h(2, 32, 128), pool, pool << 1, None, None),
+       status(pkv.pkv_rope_append_axes, ctx, h(2, 32, 128), h(2, 8, 128), h(2, 8, 128), i(2, 2), [64], i(2), h(2, 32, 128), pool, pool << 1, None, None))
+assert got == want, got
+"""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, env=env, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
