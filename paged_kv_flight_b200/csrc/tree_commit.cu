@@ -14,20 +14,22 @@
 // What bounds it: latency (the moved rows are a few MB at most: a chain of
 // dependent loads, lengths and path, table entries, rows, and one launch).  The
 // places of the first 128 moves stay in shared memory from the check to the
-// move.  One CTA per request and kv head; the CTAs of a request are a cluster:
-// each arrives at its barrier once it has read seq_lens, and one waits there
-// before it writes lens_out, which may be the same.
+// move.  One CTA takes 8 kv heads of a request (with a CTA for each head the
+// launch of 2048 of them bounded a batch of 256), the CTAs of a request are a
+// cluster: each arrives at its barrier once it has read seq_lens, and one waits
+// there before it writes lens_out, which may be the same.
 //
-// Measured (B200): 4 requests, paths of 5, bf16: 4.8 us on the device (5.6 with
-// the places looked up again for every move); 256 requests, paths of 8, 8 kv
-// heads, E4M3: 10.3 us (12.3).
+// Measured (B200, a call among others): 256 requests, paths of 8, 8 kv heads, E4M3,
+// 6.2 us (8.2 with a CTA a head); 4 requests, paths of 5, bf16, 4.9, the host.
 #include "tree_params.h"
 #include "pkv_device.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kCommitThreads = 128;
+constexpr int kCommitThreads = 256;
+constexpr int kCommitHeads = 8;             // kv heads of a CTA
+constexpr int kCommitRows = 4;              // rows that a thread holds at once
 
 // 4 E4M3 codes of one scale stored under another: fl32(code * from) / to.
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float from, float to)
@@ -46,12 +48,13 @@ __device__ __forceinline__ uint4 rescale16(uint4 v, float from, float to)
 }
 
 // Grid (cluster size, batch): rank blockIdx.x of request blockIdx.y takes the
-// kv heads rank, rank + cluster size, ...
+// kv heads 8 rank .., 8 (rank + cluster size) .., and so on.
 template <int D, bool FP8>
 __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeCommitParams p)
 {
     constexpr int CHUNKS = D * (FP8 ? 1 : 2) / 16;          // 16-byte pieces of a row
-    constexpr int ROWS = kCommitThreads / CHUNKS;           // rows per wave
+    constexpr int STEP = kCommitThreads / CHUNKS / kCommitHeads;     // rows of all threads together
+    constexpr int ROWS = STEP * kCommitRows;                // rows per wave
     __shared__ int2 s_move[kCommitThreads];                 // rows (page x P + place) that entry j goes from and to
     const int b = blockIdx.y, tid = threadIdx.x;
     const int32_t* path = p.path + (size_t)b * p.path_stride;
@@ -82,41 +85,47 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeC
     asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     if (bad && blockIdx.x == 0) atomicOr(p.err, bad);
     if (good) {
-        const int chunk = tid % CHUNKS, r = tid / CHUNKS;
-        for (int kvh = blockIdx.x; kvh < p.Hkv; kvh += gridDim.x) {
+        const int chunk = tid % CHUNKS, head = tid / CHUNKS % kCommitHeads, r = tid / CHUNKS / kCommitHeads;
+        for (int h0 = blockIdx.x * kCommitHeads; h0 < p.Hkv; h0 += gridDim.x * kCommitHeads) {
+            const int kvh = h0 + head;
             for (int j0 = 0; j0 < n; j0 += ROWS) {
-                const int j = j0 + r;
-                int2 at = make_int2(0, 0);
-                if (j < n) {
-                    if (j < kCommitThreads) {
-                        at = s_move[j];
-                    } else {
-                        const int from = L + path[j], to = L + j;
-                        at = make_int2(table[from >> p.page_shift] * p.P + (from & (p.P - 1)),
-                                       table[to >> p.page_shift] * p.P + (to & (p.P - 1)));
+                uint4 k[kCommitRows], v[kCommitRows];
+                size_t to[kCommitRows];
+                bool moves[kCommitRows];
+#pragma unroll
+                for (int i = 0; i < kCommitRows; ++i) {
+                    const int j = j0 + r + i * STEP;
+                    int2 at = make_int2(0, 0);
+                    if (j < n && kvh < p.Hkv) {
+                        if (j < kCommitThreads) {
+                            at = s_move[j];
+                        } else {
+                            const int src = L + path[j], dst = L + j;
+                            at = make_int2(table[src >> p.page_shift] * p.P + (src & (p.P - 1)),
+                                           table[dst >> p.page_shift] * p.P + (dst & (p.P - 1)));
+                        }
                     }
-                }
-                const bool moves = at.x != at.y;
-                uint4 k, v;
-                size_t to = 0;
-                if (moves) {
+                    moves[i] = at.x != at.y;
+                    if (!moves[i]) continue;
                     const int p0 = at.x >> p.page_shift, p1 = at.y >> p.page_shift;
                     const size_t from = (((size_t)p0 * p.Hkv + kvh) * p.P + (at.x & (p.P - 1))) * CHUNKS + chunk;
-                    to = (((size_t)p1 * p.Hkv + kvh) * p.P + (at.y & (p.P - 1))) * CHUNKS + chunk;
-                    k = reinterpret_cast<const uint4*>(p.k_pool)[from];
-                    v = reinterpret_cast<const uint4*>(p.v_pool)[from];
+                    to[i] = (((size_t)p1 * p.Hkv + kvh) * p.P + (at.y & (p.P - 1))) * CHUNKS + chunk;
+                    k[i] = reinterpret_cast<const uint4*>(p.k_pool)[from];
+                    v[i] = reinterpret_cast<const uint4*>(p.v_pool)[from];
                     if (FP8 && p0 != p1) {
                         const size_t s0 = (size_t)p0 * p.Hkv + kvh, s1 = (size_t)p1 * p.Hkv + kvh;
                         const float k0 = __ldg(&p.k_scale[s0]), k1 = __ldg(&p.k_scale[s1]), v0 = __ldg(&p.v_scale[s0]),
                                     v1 = __ldg(&p.v_scale[s1]);
-                        if (k0 != k1) k = rescale16(k, k0, k1);
-                        if (v0 != v1) v = rescale16(v, v0, v1);
+                        if (k0 != k1) k[i] = rescale16(k[i], k0, k1);
+                        if (v0 != v1) v[i] = rescale16(v[i], v0, v1);
                     }
                 }
                 __syncthreads();
-                if (moves) {
-                    reinterpret_cast<uint4*>(p.k_pool)[to] = k;
-                    reinterpret_cast<uint4*>(p.v_pool)[to] = v;
+#pragma unroll
+                for (int i = 0; i < kCommitRows; ++i) {
+                    if (!moves[i]) continue;
+                    reinterpret_cast<uint4*>(p.k_pool)[to[i]] = k[i];
+                    reinterpret_cast<uint4*>(p.v_pool)[to[i]] = v[i];
                 }
             }
         }
@@ -128,8 +137,12 @@ __global__ void __launch_bounds__(kCommitThreads) tree_commit_kernel(const TreeC
 template <int D, bool FP8>
 cudaError_t launch_t(const TreeCommitParams& p, cudaStream_t stream)
 {
-    int size = 1;                       // CTAs per request: a power of two up to the kv heads, at most 8
-    while (size * 2 <= p.Hkv && size < 8) size *= 2;
+    int size = 1;                       // CTAs per request: a power of two, at most 8
+    while (size < 8 && size * kCommitHeads < p.Hkv) size *= 2;
+    if (size == 1) {                    // a cluster of one needs no attribute
+        tree_commit_kernel<D, FP8><<<dim3(1, (unsigned)p.batch), kCommitThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)size, (unsigned)p.batch);
     cfg.blockDim = dim3(kCommitThreads);
