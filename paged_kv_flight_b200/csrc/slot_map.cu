@@ -21,13 +21,14 @@
 // kernel, then takes its own rows.  The parents of its rows and of those before
 // them are read into shared memory while the lengths are on their way, so that
 // the walks up the trees do not go to L2 step by step.  pages_out and free_left
-// may be the inputs that other CTAs still read: they are written behind the
-// cluster's barrier.  The sums saturate (whatever the lengths, 32 bits hold
-// them).
+// may be the inputs that other CTAs still read: each CTA arrives at the cluster's
+// barrier once it has read them, and the one that writes them waits there.  The
+// sums saturate (whatever the lengths, 32 bits hold them).
 //
-// Measured (B200): 256 requests, 4.7 thousand tokens in trees of up to 32, 8.0 us
-// on the device (9.0 with the walks in L2 and a grid of small CTAs); 4 requests
-// of one token, 5.7 us (7.0).
+// Measured (B200): 256 requests, 4.7 thousand tokens in trees of up to 32, 7.5 us
+// a call among others (8.2 with the barrier at the end; 9.0 on the device against
+// 8.0 with the walks in L2 and a grid of small CTAs); 4 requests of one token, 5.5,
+// most of it the host's.
 #include "tree_params.h"
 
 namespace pkv {
@@ -76,7 +77,9 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
     constexpr int WARPS = THREADS / 32;
     extern __shared__ int s_dyn[];
     int* const s_cu = s_dyn;                   // [batch + 1] first row of each request, at most n_tokens
-    int* const s_first = s_dyn + p.batch + 1;  // [batch] pages taken before it; -1: not served, or out of range
+    int* const s_first = s_dyn + p.batch + 1;  // [batch] pages taken before it; -1: not served, -2: out of range
+    int* const s_len = s_first + p.batch;      // [batch] L
+    int* const s_held = s_len + p.batch;       // [batch] pages held
     __shared__ unsigned s_tok[WARPS], s_pg[WARPS];
     __shared__ int s_par[2 * THREADS];         // parents of this CTA's rows and of THREADS rows before them
     __shared__ int s_taken, s_err;
@@ -135,7 +138,9 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
         const unsigned after = sat_add(pg, min((unsigned)r.take, pg_top), pg_top);
         const bool served = r.take == 0 || after <= (unsigned)count;
         s_cu[b] = (int)min(tok, (unsigned)p.n_tokens);
-        s_first[b] = !r.ok || !served ? -1 : (int)min(pg, (unsigned)count);
+        s_first[b] = !r.ok ? -2 : !served ? -1 : (int)min(pg, (unsigned)count);
+        s_len[b] = r.L;
+        s_held[b] = r.held;
         if (!r.ok) err |= kErrLength;
         if (!served) err |= kErrNoPages;
         tok = sat_add(tok, min((unsigned)r.n, tok_top), tok_top);
@@ -152,6 +157,8 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
         if (err) atomicOr(&s_err, err);
     }
     __syncthreads();
+    // the inputs that may be outputs are read: whoever writes them waits for this
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
     if (rank == 0) {
         for (int b = tid; b <= p.batch; b += THREADS) p.cu_q[b] = s_cu[b];
         if (tid == 0 && s_err) atomicOr(p.err, s_err);
@@ -173,9 +180,9 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
                     if (s_cu[mid] <= row) l = mid;
                     else h = mid;
                 }
-                const int b = l, start = s_cu[b], i = row - start, L = p.seq_lens[b], held = p.pages_held[b];
+                const int b = l, start = s_cu[b], i = row - start, L = s_len[b], held = s_held[b];
                 const int first = s_first[b];
-                const bool in_range = first >= 0 || read_request(p, b).ok;
+                const bool in_range = first != -2;
                 const int at = (int)min((long long)L + i, kMaxTreeKeys);      // of a request in range: L + i
                 const int lp = max(at, 0) >> p.page_shift, place = at & (p.P - 1);
                 int page = -1;
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
     if (bad) atomicOr(p.err, bad);
 
     // ---- the outputs that may be inputs: once no CTA reads them any more
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     if (rank) return;
     for (int b = lo; b < hi; ++b) {
         if (per > 1) r = read_request(p, b);
@@ -251,13 +258,13 @@ template <int THREADS>
 cudaError_t launch_t(const SlotMapParams& p, int ctas, cudaStream_t stream)
 {
     if (ctas == 1) {                 // a cluster of one needs no attribute, and starts cheaper on the host
-        slot_map_kernel<THREADS><<<1, THREADS, (2 * (size_t)p.batch + 1) * sizeof(int), stream>>>(p);
+        slot_map_kernel<THREADS><<<1, THREADS, (4 * (size_t)p.batch + 1) * sizeof(int), stream>>>(p);
         return cudaGetLastError();
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = (2 * (size_t)p.batch + 1) * sizeof(int);
+    cfg.dynamicSmemBytes = (4 * (size_t)p.batch + 1) * sizeof(int);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -273,7 +280,7 @@ template <int THREADS>
 cudaError_t prepare_t()
 {
     return cudaFuncSetAttribute(slot_map_kernel<THREADS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (2 * kMaxBatch + 1) * (int)sizeof(int));
+                                (4 * kMaxBatch + 1) * (int)sizeof(int));
 }
 
 }  // namespace
