@@ -385,7 +385,7 @@ pkv_status pkv_rope_append_axes(pkv_ctx* ctx, const void* q, const void* k_new, 
  *   q, out     [n_tokens][Hq][d] bf16; rows outside every request are left
  *              as they were.  q and out may not overlap.
  *   tree_mask  [n_tokens][mask_words] 32-bit words, T_b <= 32 mask_words
- * bf16 or E4M3 pools (scales as for pkv_decode_attn, finite).  The cache is read
+ * bf16 or E4M3 pools (scales as for pkv_decode_attn, finite, >= 0).  The cache is read
  * once for every 2 * (128 / G) new tokens of a request.  Weights are rounded to
  * bf16 for the product with V (2^-8 of each at most), sums are fp32.  What K and V
  * of new tokens hold that a row does not see, NaN and infinity included, does not

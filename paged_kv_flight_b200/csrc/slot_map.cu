@@ -26,9 +26,9 @@
 // sums saturate (whatever the lengths, 32 bits hold them).
 //
 // Measured (B200): 256 requests, 4.7 thousand tokens in trees of up to 32, 7.5 us
-// a call among others (8.2 with the barrier at the end; 9.0 on the device against
-// 8.0 with the walks in L2 and a grid of small CTAs); 4 requests of one token, 5.5,
-// most of it the host's.
+// a call among others (8.2 with the barrier at the end; before that 8.0 on the
+// device, and 9.0 with the walks in L2 and a grid of small CTAs); 4 requests of one
+// token, 5.5, most of it the host's.
 #include "tree_params.h"
 
 namespace pkv {

@@ -700,7 +700,6 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
             __syncwarp();
         }
     } else if (warp < 12) {
-        
         // ---- softmax and output: row r of stream st
         const int st = (warp - 4) >> 2, quarter = warp & 3, r = 32 * quarter + lane;
         const int rtok = (r * p.g_inv) >> 16, g = r - rtok * p.G;
