@@ -386,8 +386,8 @@ pkv_status pkv_rope_append_axes(pkv_ctx* ctx, const void* q, const void* k_new, 
  *              as they were.  q and out may not overlap.
  *   tree_mask  [n_tokens][mask_words] 32-bit words, T_b <= 32 mask_words
  * bf16 or E4M3 pools (scales as for pkv_decode_attn, finite, >= 0).  The cache is read
- * once for every 2 * (128 / G) new tokens of a request.  Weights are rounded to
- * bf16 for the product with V (2^-8 of each at most), sums are fp32.  What K and V
+ * once for every 2 * (128 / G) new tokens of a request.  Weights keep 2^-15 of
+ * themselves in the product with V (two bf16 terms), sums are fp32.  What K and V
  * of new tokens hold that a row does not see, NaN and infinity included, does not
  * touch the row.  The work is split over
  * the SMs along the cache, and partial results are merged by log-sum-exp in a

@@ -30,18 +30,19 @@
 // Warps: 0 and 2 load Q, K and V (TMA), 1 issues the MMAs, 4 .. 11 softmax and
 // output, one thread per row; for E4M3 pools 12 .. 15 turn the codes into
 // bf16 tiles (exact; the scales of a page and head go into the scores and the
-// weights in fp32).  P is rounded to bf16 for the matrix product, each weight off
-// by at most 2^-8 of itself, as the output is; a second bf16 term for what is left
-// would be half as many MMAs again.
+// weights in fp32).  P goes into the matrix product as two bf16 terms, cut and
+// rounded, that are off by at most 2^-15 of a weight together: with one term (half
+// as many P V MMAs) each weight is off by up to 2^-8, as much again as the output's
+// own rounding, and a row that sees one key does not get its V back.
 //
-// What bounds it, and what it measured (B200, us a call): long caches, memory (8
-// requests of 32k to 128k tokens, 8 new ones each, 2.28 GB: 361, 98% of the
-// measured copy; 64 requests of 128 to 4096, 9 to 16 new ones, 555 MB: 113, 76%);
-// large trees, the chain of a tile, S, softmax, P V and the handovers between
-// them, of which tensor memory holds two at d = 128 (48 requests, 33 to 64 new
-// tokens of 64 heads: 164, where the products alone take 52); E4M3 caches, the
-// same beside the conversion (64 requests, 391 MB: 159); a few short requests,
-// latency (4 requests: 11.8).
+// What bounds it, and what it measured (B200, us a call): the chain of a tile, S,
+// softmax, P V and the handovers between them, of which tensor memory holds two at
+// d = 128; the second term of P lengthens it by 512 cycles.  Long caches (8 requests
+// of 32k to 128k tokens, 8 new ones each, 2.28 GB: 468, 75% of the measured copy; 396
+// with one term), serving batches (64 requests of 128 to 4096, 9 to 16 new ones, 555
+// MB: 139; 119), large trees (48 requests, 33 to 64 new tokens of 64 heads: 201, where
+// the products alone take 78; 169), E4M3 caches, beside the conversion (64 requests,
+// 391 MB: 187; 167); a few short requests, latency (4 requests: 12.2).
 #include "tree_params.h"
 #include "pkv_device.cuh"
 #include "umma.cuh"
@@ -60,10 +61,12 @@ constexpr int kMaxSlots = 8;
 constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // Cost of a tile for the cut, and of an item besides its tiles (Q, the masked
 // tile, the merge of the streams, the output).  Fitted over the CTAs of three
-// workloads: 3900 cycles a tile in row mode, 1950 in key mode, 8.7 to 12 thousand
-// an item.  Cut by tiles alone, the slowest CTA took 1.5 to 2 times the mean (297
-// us against 184 for large trees); with 7 or 12 for the item they took 3 and 2%
-// longer.
+// workloads at d = 128 in bf16, with P in one term: 3900 cycles a tile in row mode,
+// 1950 in key mode, 8.7 to 12 thousand an item.  Cut by tiles alone, the slowest CTA
+// took 1.5 to 2 times the mean (297 us against 184 for large trees); with 7 or 12 for
+// the item they took 3 and 2% longer.  With P in two terms a tile takes about a
+// quarter more in both modes, and 7, 8 and 9 for the item are alike within 1%, for
+// E4M3 caches too.
 constexpr int kCostRowShift = 2, kCostKeyShift = 1, kCostItem = 9;
 constexpr int kCostRow = 1 << kCostRowShift, kCostKey = 1 << kCostKeyShift;
 // How far a row's maximum may pass its reference, in powers of two, before the
@@ -308,14 +311,29 @@ __device__ __forceinline__ void tmem_scale16(uint32_t col, float alpha)
     }
 }
 
+// Keys of a chunk of the softmax pass, and the column of the first terms of P of
+// 16 keys (the second ones are half a chunk behind).
+template <bool FP8>
+constexpr int kChunk = FP8 ? 32 : 64;
+template <bool FP8>
+__device__ __forceinline__ constexpr uint32_t p_col(int kk)
+{
+    constexpr int N = kChunk<FP8>;
+    return (uint32_t)(16 * kk / N * N + 16 * kk % N / 2);
+}
+
 // One pass over the row's S, 64 keys (E4M3: 32) at a time in a loop that is not unrolled
 // (unrolled, the code was over 64 KB, and fetching it made every warp of the SM
 // several times slower).  A chunk's maximum is taken
 // while its scores are in registers; the reference m, a whole number, moves
 // only when some row of the warp passes it by more than 2^24, and then what was
 // made with the old one (O of this stream, the tile's chunks of P, l) is
-// multiplied by a power of two, which is exact.  P = 2^(s - m) goes back as
-// bf16 over the S columns already read, keys 2i and 2i + 1 in column i.
+// multiplied by a power of two, which is exact.  P = 2^(s - m) goes back over the
+// chunk's own S columns, just read, as two bf16 terms: of N columns the first N / 2
+// hold the first terms, keys 2i and 2i + 1 in column i, the others the second.
+// The first term is the weight's upper half, cut (no conversion, and the rest,
+// below 2^-7 of the weight, is an exact difference); the second is the rest rounded.
+// l is summed from the fp32 weights, of which the two terms leave 2^-15 at most.
 //
 // f: score scale in log2 units.  E4M3: `scales` of lane k holds the K scale of
 // the tile's page k, of lane 8 + k its V scale; pages are 1 << shift keys.
@@ -323,7 +341,7 @@ template <int D, bool FP8>
 __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool first, float f, float scales, int shift,
                                              float& m, float& l)
 {
-    constexpr int N = FP8 ? 32 : 64;                          // keys of a chunk
+    constexpr int N = kChunk<FP8>;
 #pragma unroll 1
     for (int k = 0; k < kTKeys / N; ++k) {
         uint32_t x[N];
@@ -359,7 +377,7 @@ __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool 
             }
             tmem_wait_st();
 #pragma unroll 1
-            for (int c0 = 0; c0 < N / 2 * k; c0 += 16) tmem_scale16<true>(scol + (uint32_t)c0, alpha);
+            for (int c0 = 0; c0 < N * k; c0 += 16) tmem_scale16<true>(scol + (uint32_t)c0, alpha);
             l *= alpha;
             m = mn;
         }
@@ -377,9 +395,19 @@ __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool 
                 uint64_t e = two(ex2(first_of(z)), ex2(second_of(z)));
                 sum[i & 1] = add2(sum[i & 1], e);
                 if (FP8) e = mul2(e, two(vs[h], vs[h]));       // the V scale goes into what P V takes, not into the sum
-                w[i] = pack_bf16(first_of(e), second_of(e));
+                x[c] = (uint32_t)e;
+                x[c + 1] = (uint32_t)(e >> 32);
+                w[i] = __byte_perm(x[c], x[c + 1], 0x7632);
             }
-            tmem_st8(scol + (uint32_t)(N / 2 * k + 8 * h), w);
+            tmem_st8(scol + (uint32_t)(N * k + 8 * h), w);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int c = 16 * h + 2 * i;
+                const float r0 = __uint_as_float(x[c]) - __uint_as_float(x[c] & 0xFFFF0000u),
+                            r1 = __uint_as_float(x[c + 1]) - __uint_as_float(x[c + 1] & 0xFFFF0000u);
+                w[i] = pack_bf16(r0, r1);
+            }
+            tmem_st8(scol + (uint32_t)(N * k + N / 2 + 8 * h), w);
         }
         const uint64_t all = add2(sum[0], sum[1]);
         l += first_of(all) + second_of(all);
@@ -670,14 +698,19 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                     if (!ok) break;
                     tmem_fence_after();
                     if (elect_one()) {
+                        // 16 keys each: both terms of P over the same V
+                        auto step = [&](int kk) {
+                            const uint32_t at = pcol + p_col<FP8>(kk);
+                            const uint64_t v = va + (uint64_t)(kk * 128);
+                            umma_bf16_ts_all(ocol, at, v, idO, kk ? 1u : later);
+                            umma_bf16_ts_all(ocol, at + (uint32_t)(kChunk<FP8> / 2), v, idO, 1u);
+                        };
                         if (steps == kTKeys / 16) {
 #pragma unroll
-                            for (int kk = 0; kk < kTKeys / 16; ++kk)        // 16 keys each
-                                umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                            for (int kk = 0; kk < kTKeys / 16; ++kk) step(kk);
                         } else {
 #pragma unroll 1
-                            for (int kk = 0; kk < steps; ++kk)
-                                umma_bf16_ts_all(ocol, pcol + (uint32_t)(8 * kk), va + (uint64_t)(kk * 128), idO, kk ? 1u : later);
+                            for (int kk = 0; kk < steps; ++kk) step(kk);
                         }
                         if (!s.row_mode || st) umma_commit(empty + 8u * vslot);
                         if (!next) umma_commit(ofin + 8u * st);

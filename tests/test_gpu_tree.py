@@ -890,3 +890,35 @@ def test_marshal_pointers(pkv):
             assert bad is None
         assert m.pointer(x[2], k, 6) == x.data_ptr() + 12 * x.element_size()
     assert m.pointer(torch.zeros(2, device=DEV, dtype=torch.uint8), 2) and m.pointer(torch.zeros(2, device=DEV), 2) is None
+
+
+@pytest.mark.parametrize("case", ATTN_CASES, ids=lambda c: f"h{c[0]}_{c[1]}_d{c[2]}_p{c[3]}_{'f8' if c[4] else 'bf'}_{c[5][0]}")
+def test_tree_attention_keeps_the_bits_of_its_weights(pkv, case):
+    """The weights go into the product with V as two bf16 terms: the first off
+    by less than 2^-7 (cut, not rounded), the second rounded to 2^-8 of that,
+    2^-15 in all; with 2^-13.6 of the fp32 scores and 2^-21 of the rest (above)
+    less than 2^-12 of A."""
+    x = _attn_inputs(case, seed=1)
+    ref, size = _attn_ref(x)
+    with _attn_ctx(pkv, x) as ctx:
+        got = _tree.values(_attn_run(pkv, ctx, _attn_device(x)))
+        _ok(pkv, ctx)
+    err = np.abs(got - ref) - (2.0 ** -8 * np.abs(ref) + 2.0 ** -12 * size)
+    assert (err <= 0).all(), (float(err.max()), int((err > 0).sum()))
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_attention_of_one_key_is_its_v(pkv, fp8):
+    """A row that sees one key has that key's V: bit for bit in bf16 (2^-15 of
+    the weight is far below half a step of V), and off by one rounding of code *
+    scale from an E4M3 cache."""
+    x = _attn_inputs((8, 2, 128, 16, fp8, [0, 0, 0], [20, 140, 1], "star"))
+    with _attn_ctx(pkv, x) as ctx:
+        out = _attn_run(pkv, ctx, _attn_device(x))
+        _ok(pkv, ctx)
+    got = _tree.values(out)
+    for b in range(3):
+        for i in range(int(x["cu"][b + 1] - x["cu"][b])):
+            want = np.repeat(x["vv"][x["table"][b, i // 16], :, i % 16], 4, axis=0)
+            err = np.abs(got[x["cu"][b] + i] - want)
+            assert (err <= (2.0 ** -8 + 2.0 ** -14 if fp8 else 0.0) * np.abs(want)).all(), (b, i, float(err.max()))
