@@ -337,8 +337,10 @@ pkv_status pkv_table_sync(const int32_t* upload, int n_changes, int batch, int m
  * no page, are served); a length, count or held value out of range, more
  * drafted tokens than 32 mask_words, or a parent that is not an earlier token
  * (slot -1, PKV_ERR_DEVICE_BOUNDS); a table or stack entry that is no page
- * (the slots in it -1); more tokens than n_tokens (the surplus dropped, cu_q
- * clipped). */
+ * (the slots in it -1); more tokens than n_tokens (the surplus has no
+ * row and cu_q is clipped; the pages are taken and entered for all tokens, so
+ * that block_tables, pages_out and free_left agree and a next step can go on;
+ * PKV_ERR_DEVICE_BOUNDS.  A count out of range takes the rows behind it so). */
 pkv_status pkv_slot_map(pkv_ctx* ctx, const int32_t* seq_lens, const int32_t* new_lens, const int32_t* parents,
                         int batch, int32_t* block_tables, int bt_stride, const int32_t* pages_held,
                         int32_t* pages_out, const int32_t* free_pages, int free_cap, const int32_t* free_count,

@@ -82,13 +82,14 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
     int* const s_held = s_len + p.batch;       // [batch] pages held
     __shared__ unsigned s_tok[WARPS], s_pg[WARPS];
     __shared__ int s_par[2 * THREADS];         // parents of this CTA's rows and of THREADS rows before them
-    __shared__ int s_taken, s_err;
+    __shared__ int s_taken, s_err, s_over;     // s_over: more tokens than rows
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, stride = gridDim.x * THREADS;
 
     if (tid == 0) {
         s_taken = 0;
         s_err = 0;
+        s_over = 0;
     }
     int row0 = rank * THREADS;
     int par[2] = {-1, -1};
@@ -149,7 +150,10 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
     }
     if (hi == p.batch && lo < hi) {
         s_cu[p.batch] = (int)min(tok, (unsigned)p.n_tokens);
-        if (tok > (unsigned)p.n_tokens) err |= kErrLength;
+        if (tok > (unsigned)p.n_tokens) {
+            err |= kErrLength;
+            s_over = 1;
+        }
     }
     if (rank == 0) {
         if (given != count && tid == 0) err |= kErrLength;
@@ -243,6 +247,21 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
         __syncthreads();
     }
     if (bad) atomicOr(p.err, bad);
+    // Pages are entered by the rows of their first new tokens.  Where tokens were
+    // dropped the pages that they were taken for are entered here (those that have
+    // rows a second time, with the same number), a warp for each request: pages_out
+    // and free_left count them, and the next step reads them from the table.  The
+    // barrier behind it keeps pages_held, which may be pages_out, as it is read here.
+    if (s_over && rank == 0) {
+        for (int b = warp; b < p.batch; b += WARPS) {
+            const int first = s_first[b], held = s_held[b];
+            if (first < 0) continue;
+            const int take = read_request(p, b).take;
+            for (int k = lane; k < take; k += 32)
+                p.block_tables[(size_t)b * p.bt_stride + held + k] = __ldg(&p.free_pages[count - 1 - (first + k)]);
+        }
+        __syncthreads();
+    }
 
     // ---- the outputs that may be inputs: once no CTA reads them any more
     asm volatile("barrier.cluster.wait.aligned;" ::: "memory");

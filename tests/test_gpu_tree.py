@@ -922,3 +922,40 @@ def test_tree_attention_of_one_key_is_its_v(pkv, fp8):
             want = np.repeat(x["vv"][x["table"][b, i // 16], :, i % 16], 4, axis=0)
             err = np.abs(got[x["cu"][b] + i] - want)
             assert (err <= (2.0 ** -8 + 2.0 ** -14 if fp8 else 0.0) * np.abs(want)).all(), (b, i, float(err.max()))
+
+
+@pytest.mark.parametrize("cap", [0, 1, 10, 60, 200])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_slot_map_more_tokens_than_rows(pkv, cap, tree, inplace):
+    """Tokens that have no row are dropped, and nothing else: the table, the
+    pages held and the stack agree with one another, as if they had rows."""
+    rng = np.random.default_rng(17)
+    x = _slot_inputs(rng, 12, 16, 0, 60, 0, 70, tree)
+    assert x["new"].sum() > 250
+    r = _tree.slot_map(x["lens"], x["new"], x["table"], x["held"], x["free"], x["count"], 16, cap, x["parents"], 3)
+    with _Ctx(pkv, 8, 2, 64, 16, False, 12, x["table"].shape[1], x["pages"]) as ctx:
+        _slot_check(_slot_call(pkv, ctx, x, cap, 3, inplace), r)
+        assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 1)
+
+
+@pytest.mark.parametrize("n", [1 << 20, 2 ** 31 - 1])
+@pytest.mark.parametrize("b", [0, 5])
+def test_slot_map_next_to_a_count_far_too_large(pkv, b, n):
+    """One count out of range takes the rows behind it, but leaves the other
+    requests' pages in a state to go on from."""
+    rng = np.random.default_rng(23)
+    x = _slot_inputs(rng, 9, 16, 0, 60, 1, 40, False)
+    x["new"][b] = 0
+    cap = int(x["new"].sum()) + 50
+    r = _tree.slot_map(x["lens"], x["new"], x["table"], x["held"], x["free"], x["count"], 16, cap)
+    start = int(r["cu"][b])
+    x["new"][b] = n
+    with _Ctx(pkv, 8, 2, 64, 16, False, 9, x["table"].shape[1], x["pages"]) as ctx:
+        g = _slot_call(pkv, ctx, x, cap, 1)
+        assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 1)
+    for k in ("table", "pages"):
+        assert np.array_equal(g[k].cpu().numpy(), r[k]), k
+    assert int(g["left"][0]) == r["left"]
+    assert g["cu"].tolist() == [int(v) for v in r["cu"][:b + 1]] + [cap] * (9 - b)
+    assert g["slots"].tolist() == r["slots"][:start].tolist() + [-1] * (cap - start)
