@@ -1064,8 +1064,8 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
                 ml[k] = p.part_ml[at];
 #pragma unroll
                 for (int e = 0; e < E / 4; ++e) v[k][e] = *reinterpret_cast<const float4*>(p.part_o + at * D + lane * E + 4 * e);
-                if (c0 + k >= n) ml[k].x = -INFINITY;
             }
+            // (the last part stands in for those behind it: the maximum is the same)
             const float mn = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m);
             const float old = m == -INFINITY ? 0.f : ex2(m - mn);
             l *= old;
@@ -1073,8 +1073,11 @@ __global__ void __launch_bounds__(kCombineThreads) tree_combine_kernel(const Tre
             for (int e = 0; e < E; ++e) acc[e] *= old;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                if (c0 + k >= n) break;
+                // A part in which the row sees nothing is (-inf, 0) and O = 0.  One whose
+                // scores are no numbers has m = -inf too, as the maximum leaves NaN out,
+                // but l and O are NaN, and stay so times 0
                 const float f = ml[k].x == -INFINITY ? 0.f : ex2(ml[k].x - mn);
-                if (f == 0.f) continue;                    // nothing of it, whatever it holds
                 l = fmaf(f, ml[k].y, l);
 #pragma unroll
                 for (int e = 0; e < E; ++e) acc[e] = fmaf(f, reinterpret_cast<const float*>(v[k])[e], acc[e]);

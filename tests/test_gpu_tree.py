@@ -959,3 +959,50 @@ def test_slot_map_next_to_a_count_far_too_large(pkv, b, n):
     assert int(g["left"][0]) == r["left"]
     assert g["cu"].tolist() == [int(v) for v in r["cu"][:b + 1]] + [cap] * (9 - b)
     assert g["slots"].tolist() == r["slots"][:start].tolist() + [-1] * (cap - start)
+
+
+# a cache long enough that its only item is cut, and one that is not
+NAN_CASES = [(8, 1, 64, 16, False, [9000], [3], "random"), (8, 1, 128, 32, True, [7000], [20], "random"),
+             (8, 2, 128, 16, False, [60, 7], [20, 33], "random")]
+
+
+@pytest.mark.parametrize("case", NAN_CASES, ids=lambda c: f"d{c[2]}_{'f8' if c[4] else 'bf'}_{c[5][0]}")
+def test_tree_attention_of_a_query_that_is_no_number(pkv, case):
+    """One NaN in a head's query makes that head's output NaN, wherever its
+    item is cut, and no other."""
+    x = _attn_inputs(case)
+    ref, size = _attn_ref(x)
+    x["q"][1, 3, 5] = float("nan")
+    with _attn_ctx(pkv, x) as ctx:
+        got = _tree.values(_attn_run(pkv, ctx, _attn_device(x)))
+        _ok(pkv, ctx)
+    assert np.isnan(got[1, 3]).all()
+    got[1, 3], ref[1, 3] = 0, 0
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + W * size).all()
+
+
+@pytest.mark.parametrize("case", NAN_CASES, ids=lambda c: f"d{c[2]}_{'f8' if c[4] else 'bf'}_{c[5][0]}")
+@pytest.mark.parametrize("which", ["one", "many", "far"])
+def test_tree_attention_of_cached_keys_that_are_no_numbers(pkv, case, which):
+    """A NaN key in the cache, a run of them longer than an item's part, and one
+    whose part lies so far below the others that its weight is 0."""
+    x = _attn_inputs(case)
+    Hq, Hkv, d, P, fp8, lens = case[:6]
+    u = x["k"].view(torch.uint8) if fp8 else x["k"]
+    nan = 0x7F if fp8 else float("nan")
+    L = lens[0]
+    if which == "far":                   # later keys: 200 times as large, along the queries
+        big = x["q"][:, 0].float().sign().sum(0).sign()
+        big[big == 0] = 1
+        for pos in range(L // 2, L):
+            x["k"][x["table"][0, pos // P], 0, pos % P] = (big * (400 if fp8 else 200)).to(x["k"].dtype)
+    for pos in range(L // 4, L // 4 + (1 if which == "one" else min(1000, L // 4))):
+        u[x["table"][0, pos // P], 0, pos % P] = nan
+    with _attn_ctx(pkv, x) as ctx:
+        got = _tree.values(_attn_run(pkv, ctx, _attn_device(x)))
+        _ok(pkv, ctx)
+    n = int(x["cu"][1])
+    assert np.isnan(got[:n, :Hq // Hkv]).all()
+    if Hkv > 1:
+        assert np.isfinite(got[:n, Hq // Hkv:]).all()
+    assert np.isfinite(got[n:]).all()
