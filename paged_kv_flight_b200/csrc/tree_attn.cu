@@ -767,10 +767,13 @@ tree_attn_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant_
                 const int at = ((s.t0 + i) << (7 - shift)) + (lane & 7);
                 return FP8 && i < s.n && lane < 16 && at * p.P < n_keys && (lane & 7) < (kTKeys >> shift) ? __ldg(&bt[at]) : -1;
             };
-            auto scale_of = [&](int page) {      // 1 where there is no page; 0 made tiny: -inf x 0 is no number
+            // 1 where there is no page.  K scales of 0 and next to it are made 1e-30
+            // (-inf, a masked score, x 0 is no number; scores move by less than
+            // 2^-60); V scales stay as they are
+            auto scale_of = [&](int page) {
                 if (!FP8 || (unsigned)page >= (unsigned)p.num_pages) return 1.f;
                 const float x = __ldg(&(lane < 8 ? p.k_scale : p.v_scale)[(size_t)page * p.Hkv + s.kvh]);
-                return x == 0.f ? 1e-30f : x;
+                return lane < 8 && x < 1e-30f ? 1e-30f : x;
             };
             float scale_next = 0.f;
             int page_next = -1;

@@ -1006,3 +1006,22 @@ def test_tree_attention_of_cached_keys_that_are_no_numbers(pkv, case, which):
     if Hkv > 1:
         assert np.isfinite(got[:n, Hq // Hkv:]).all()
     assert np.isfinite(got[n:]).all()
+
+
+@pytest.mark.parametrize("case", [(8, 2, 128, 16, True, [100, 0], [9, 33], "random"),
+                                  (8, 1, 64, 16, True, [4000], [5], "random")], ids=["short", "cut"])
+@pytest.mark.parametrize("tiny", [0.0, 1e-44])
+def test_tree_attention_scales_of_zero(pkv, case, tiny):
+    """K scales of 0 (or the smallest numbers): every key weighs the same.  V
+    scales of 0: the output is 0, not something small."""
+    x = _attn_inputs(case)
+    for zero in ("k", "v"):
+        y = dict(x, **{zero + "s": torch.full_like(x[zero + "s"], tiny), zero + "v": x[zero + "v"] * 0.0})
+        ref, size = _attn_ref(y)
+        with _attn_ctx(pkv, y) as ctx:
+            out = _attn_run(pkv, ctx, _attn_device(y))
+            _ok(pkv, ctx)
+        if zero == "v":
+            assert (out.abs() <= 448 * tiny).all(), float(out.abs().max())
+        else:
+            _attn_near(out, ref, size)
