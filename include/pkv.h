@@ -334,7 +334,10 @@ pkv_status pkv_table_sync(const int32_t* upload, int n_changes, int batch, int m
  * Device-side errors, each sticky in the error word: a request whose pages
  * the stack cannot cover keeps pages_held, its tokens get slot -1 and no page
  * is taken for it (PKV_ERR_OOM; requests before it, and later ones that need
- * no page, are served); a length, count or held value out of range, more
+ * no page, are served), and the table entries of the pages it lacks become -1, so
+ * that the attention leaves their keys out and pkv_tree_commit refuses a path
+ * through them (its tokens are not stored anywhere: the path to give it is empty;
+ * the same for a request with more tokens than its table or mask_words hold); a length, count or held value out of range, more
  * drafted tokens than 32 mask_words, or a parent that is not an earlier token
  * (slot -1, PKV_ERR_DEVICE_BOUNDS); a table or stack entry that is no page
  * (the slots in it -1); more tokens than n_tokens (the surplus has no

@@ -58,6 +58,13 @@ __device__ __forceinline__ Request read_request(const SlotMapParams& p, int b)
     return r;
 }
 
+// The pages that a request lacks, as far as the table goes, also where it takes none.
+__device__ __forceinline__ int wanted(const SlotMapParams& p, const Request& r)
+{
+    if (r.L < 0 || r.n == 0 || r.held < 0 || r.held > p.bt_stride || (long long)r.held * p.P < r.L) return 0;
+    return max(0, (int)min(((long long)r.L + r.n + p.P - 1) >> p.page_shift, (long long)p.bt_stride) - r.held);
+}
+
 __device__ __forceinline__ unsigned sat_add(unsigned a, unsigned b, unsigned top) { return min(a + b, top); }
 
 // Inclusive scan over a warp of sums that saturate at `top` (below 2^31).
@@ -82,14 +89,14 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
     int* const s_held = s_len + p.batch;       // [batch] pages held
     __shared__ unsigned s_tok[WARPS], s_pg[WARPS];
     __shared__ int s_par[2 * THREADS];         // parents of this CTA's rows and of THREADS rows before them
-    __shared__ int s_taken, s_err, s_over;     // s_over: more tokens than rows
+    __shared__ int s_taken, s_err, s_rare;     // s_rare: the table needs more than its rows write
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x, stride = gridDim.x * THREADS;
 
     if (tid == 0) {
         s_taken = 0;
         s_err = 0;
-        s_over = 0;
+        s_rare = 0;
     }
     int row0 = rank * THREADS;
     int par[2] = {-1, -1};
@@ -144,6 +151,7 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
         s_held[b] = r.held;
         if (!r.ok) err |= kErrLength;
         if (!served) err |= kErrNoPages;
+        if (!served || !r.ok) s_rare = 1;
         tok = sat_add(tok, min((unsigned)r.n, tok_top), tok_top);
         pg = after;
         if (served && r.take > 0) taken = (int)pg;   // the sums only grow: the last one served is the largest
@@ -152,7 +160,7 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
         s_cu[p.batch] = (int)min(tok, (unsigned)p.n_tokens);
         if (tok > (unsigned)p.n_tokens) {
             err |= kErrLength;
-            s_over = 1;
+            s_rare = 1;
         }
     }
     if (rank == 0) {
@@ -251,14 +259,16 @@ __global__ void __launch_bounds__(THREADS) slot_map_kernel(const SlotMapParams p
     // dropped the pages that they were taken for are entered here (those that have
     // rows a second time, with the same number), a warp for each request: pages_out
     // and free_left count them, and the next step reads them from the table.  The
-    // barrier behind it keeps pages_held, which may be pages_out, as it is read here.
-    if (s_over && rank == 0) {
+    // entries of pages that a request did not get name none, whatever was there.
+    // The barrier behind it keeps pages_held, which may be pages_out, as it is read
+    // here.
+    if (s_rare && rank == 0) {
         for (int b = warp; b < p.batch; b += WARPS) {
-            const int first = s_first[b], held = s_held[b];
-            if (first < 0) continue;
-            const int take = read_request(p, b).take;
-            for (int k = lane; k < take; k += 32)
-                p.block_tables[(size_t)b * p.bt_stride + held + k] = __ldg(&p.free_pages[count - 1 - (first + k)]);
+            const Request x = read_request(p, b);
+            const int first = s_first[b], n = wanted(p, x);
+            for (int k = lane; k < n; k += 32)
+                p.block_tables[(size_t)b * p.bt_stride + x.held + k] =
+                    first >= 0 ? __ldg(&p.free_pages[count - 1 - (first + k)]) : -1;
         }
         __syncthreads();
     }

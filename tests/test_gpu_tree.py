@@ -1025,3 +1025,60 @@ def test_tree_attention_scales_of_zero(pkv, case, tiny):
             assert (out.abs() <= 448 * tiny).all(), float(out.abs().max())
         else:
             _attn_near(out, ref, size)
+
+
+def test_slot_map_clears_the_entries_it_does_not_fill(pkv):
+    """Entries that a request would have needed and did not get name no page
+    afterwards, whatever an earlier use of the row left there: the attention
+    leaves their keys out and the commit refuses a path through them."""
+    rng = np.random.default_rng(31)
+    gen = torch.Generator().manual_seed(31)
+    P, stride, pages = 16, 8, 40
+    lens, new = np.array([20, 20, 40, 5, 30]), np.array([30, 30, 70, 9, 120])   # 2: more than the mask's words; 4: past the table
+    held = np.array([2, 2, 3, 1, 2])
+    order = rng.permutation(pages).astype(np.int32)
+    table = np.full((5, stride), -1, np.int32)
+    for b, at in enumerate((0, 2, 4, 7, 8)):
+        table[b, :held[b]] = order[at:at + held[b]]
+    table[1, 2:] = table[0, 0]                       # stale: pages of others
+    table[2, 3:] = table[0, 1]
+    table[4, 2:] = table[3, 0]
+    free = order[20:22]                              # enough for request 0 alone
+    par = sum((_tree.parents_of(rng, int(n)) for n in new), [])
+    n = int(new.sum())
+    k, v, _, _, kv, vv = _tree.pools(gen, pages, 2, P, 64, False)
+    dk, dv, dl, dt = k.to(DEV), v.to(DEV), _i(lens), _i(table)
+    cu, slots, pos, mask = _i([0] * 6), _i([0] * n), _i([0] * n), _i([[0] * 2] * n)
+    pages_out, left, out = _i([0] * 5), _i([0]), torch.zeros(n, 8, 64, dtype=torch.bfloat16, device=DEV)
+    q = torch.randn(n, 8, 64, generator=gen).to(torch.bfloat16)
+    with _Ctx(pkv, 8, 2, 64, P, False, 5, stride, pages) as ctx:
+        pkv.pkv_slot_map(ctx, dl, _i(new), dt, _i(held), _i(free), _i([2]), cu, slots, pos, pages_out, left,
+                         parents=_i(par), tree_mask=mask)
+        assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 1 | 16)
+        want = table.copy()
+        want[0, 2:4] = free[::-1]
+        want[1, 2:4] = -1
+        want[2, 3:7] = -1
+        want[4, 2:8] = -1
+        assert np.array_equal(dt.cpu().numpy(), want)
+        assert pages_out.tolist() == [4, 2, 3, 1, 2] and int(left[0]) == 0
+        s = slots.cpu().numpy()
+        assert (s[:30] >= 0).all() and (s[30:130] == -1).all() and (s[130:139] >= 0).all() and (s[139:] == -1).all()
+        # the attention: request 1 sees what its held pages hold
+        pkv.pkv_decode_attn_tree(ctx, q.to(DEV), dk, dv, None, None, dt, dl, cu, mask, out)
+        assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 1 | 2)
+        m = mask.cpu().numpy().copy()
+        m[30:60, 0] &= (1 << 12) - 1                 # keys 20 .. 31 of it
+        m[30:60, 1] = 0
+        clip = want.copy()
+        clip[1, 2:4] = 0
+        ref, size = _tree.attention(_tree.values(q)[:60], kv, vv, lens[:2], np.array([0, 30, 60]), clip[:2], m[:60], P, 4)
+        _attn_near(out[:60], ref, size)
+        # the commit: a path into the missing pages is refused, and moves nothing
+        path, plen = _i([[1, 3, 6], [1, 3, 14], [1, 2, 60], [0, 1, 2], [0, 2, 90]]), _i([3] * 5)
+        lens_out = _i([0] * 5)
+        pkv.pkv_tree_commit(ctx, dk, dv, None, None, dt, dl, path, plen, lens_out)
+        assert _status(pkv, ctx) == (pkv.PKV_ERR_DEVICE_BOUNDS, 2)
+        assert lens_out.tolist() == [23, 20, 40, 8, 30]
+        same = np.setdiff1d(np.arange(pages), want[0, :4])
+        assert torch.equal(dk.cpu()[same], k[same]) and torch.equal(dv.cpu()[same], v[same])
