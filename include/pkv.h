@@ -370,9 +370,10 @@ pkv_status pkv_slot_map(pkv_ctx* ctx, const int32_t* seq_lens, const int32_t* ne
  *                pkv_slot_map writes them; -1 skips the token (q_out, too, is
  *                left as it was).  A slot outside the pools sets the error
  *                word and is skipped; two tokens of one slot race for it.
- * Rotation in fp32 from angles reduced in fp64 (far positions keep their
- * fraction), rounded once to the storage type; E4M3 pools as for
- * pkv_rope_append.  n_tokens == 0 is a no-op. */
+ * The rotation and both kinds of pools are those of pkv_rope_append, fp64 from
+ * the angles on and one rounding to the storage type (E4M3: of the quotient):
+ * the same token at the same position is stored as the same bits by either
+ * call.  n_tokens == 0 is a no-op. */
 pkv_status pkv_rope_append_axes(pkv_ctx* ctx, const void* q, const void* k_new, const void* v_new, int n_tokens,
                                 const int32_t* positions, int n_axes, const int* sections, int interleaved,
                                 const int32_t* slots, void* q_out, void* k_pool, void* v_pool,

@@ -1082,3 +1082,57 @@ def test_slot_map_clears_the_entries_it_does_not_fill(pkv):
         assert lens_out.tolist() == [23, 20, 40, 8, 30]
         same = np.setdiff1d(np.arange(pages), want[0, :4])
         assert torch.equal(dk.cpu()[same], k[same]) and torch.equal(dv.cpu()[same], v[same])
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,P,fp8", [(8, 2, 64, 16, False), (32, 8, 128, 32, False), (8, 2, 64, 16, True),
+                                            (16, 4, 128, 64, True)])
+def test_rope_append_axes_stores_what_the_other_appends_store(pkv, Hq, Hkv, d, P, fp8):
+    """One axis: the bits of pkv_rope_append_varlen, so that a cache filled by
+    both calls is the one that either would have made; and several axes of one
+    position are one axis.  Zeros, infinities, NaN and the ends of the type too."""
+    rng = np.random.default_rng(d + Hq)
+    gen = torch.Generator().manual_seed(d)
+    B = 40
+    lens, new = rng.integers(0, 60000, B), rng.integers(1, 60, B)
+    stride = 60100 // P + 1
+    table, page = np.zeros((B, stride), np.int32), 0
+    slots, pos = [], []
+    for b in range(B):
+        for k in range(int(lens[b]) // P, (int(lens[b]) + int(new[b]) - 1) // P + 1):
+            table[b, k] = page
+            page += 1
+        at = np.arange(lens[b], lens[b] + new[b])
+        slots += (table[b, at // P] * P + at % P).tolist()
+        pos += at.tolist()
+    n = len(pos)
+    k, v, ks, vs, _, _ = _tree.pools(gen, page, Hkv, P, d, fp8)
+    q, kn, vn = (torch.randn(n, h, d, generator=gen).to(torch.bfloat16) for h in (Hq, Hkv, Hkv))
+    for t in (q, kn):
+        for i, x in enumerate((0.0, -0.0, float("inf"), float("nan"), 1e-39, -3e38, 3.39e38)):
+            t[3 * i] = x
+            t[3 * i + 1, :, ::3] = x
+            t[3 * i + 2, :, d // 2:] = x
+    if fp8:                              # scales at the ends of their type
+        for s in (ks, vs):
+            s[1], s[2], s[3] = 0.0, 1e-42, 3e38
+    cu = np.concatenate([[0], np.cumsum(new)])
+
+    def dev():
+        return [t.to(DEV, copy=True) for t in (q, kn, vn, k, v)] + [None if s is None else s.to(DEV) for s in (ks, vs)]
+
+    with _Ctx(pkv, Hq, Hkv, d, P, fp8, 64, stride, page, base=5e5) as ctx:
+        a = dev()
+        pkv.pkv_rope_append_varlen(ctx, *a, _i(table), _i(lens), _i(cu))
+        b = dev()
+        pkv.pkv_rope_append_axes(ctx, b[0], b[1], b[2], _i(pos)[None], [d // 2], _i(slots), b[0], *b[3:])
+        c = dev()
+        out = torch.zeros_like(c[0])
+        pkv.pkv_rope_append_axes(ctx, c[0], c[1], c[2], _i([pos] * 3), [d // 2 - 20, 10, 10], _i(slots), out, *c[3:],
+                                 interleaved=True)
+        c[0] = out
+        _ok(pkv, ctx)
+    for i, name in ((0, "q"), (3, "k"), (4, "v")):
+        want = a[i].view(torch.uint8)
+        for got in (b[i], c[i]):
+            diff = int((got.view(torch.uint8) != want).sum())
+            assert diff == 0, (name, diff, want.numel())
