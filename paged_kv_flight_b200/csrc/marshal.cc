@@ -13,7 +13,8 @@ namespace {
 // pointer(x, kind, size, ...): the device address of a contiguous CUDA tensor
 // of the kind's element type and these sizes (-1: any; none given: any shape),
 // or None: then the caller looks closer.
-// kind 0: int32, 1: bf16, 2: a pool (bf16, uint8 or E4M3 codes), 3: float32.
+// kind 0: int32, 1: bf16, 2: a pool (bf16, uint8 or E4M3 codes), 3: float32; plus
+// 4 (g + 1) where only tensors on cuda:g will do.
 PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t n)
 {
     if (n < 2) {
@@ -22,14 +23,15 @@ PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t n)
     }
     if (!THPVariable_CheckExact(args[0])) Py_RETURN_NONE;
     const at::Tensor& t = THPVariable_Unpack(args[0]);
-    const long kind = PyLong_AsLong(args[1]);
-    if (kind == -1 && PyErr_Occurred()) return nullptr;
+    const long code = PyLong_AsLong(args[1]), kind = code & 3, device = (code >> 2) - 1;
+    if (code == -1 && PyErr_Occurred()) return nullptr;
     const at::ScalarType s = t.scalar_type();
     const bool type = kind == 0   ? s == at::kInt
                       : kind == 1 ? s == at::kBFloat16
                       : kind == 2 ? s == at::kBFloat16 || s == at::kByte || s == at::kFloat8_e4m3fn
                                   : kind == 3 && s == at::kFloat;
     if (!type || !t.is_cuda() || t.layout() != at::kStrided || !t.is_contiguous()) Py_RETURN_NONE;
+    if (device >= 0 && t.get_device() != device) Py_RETURN_NONE;
     if (n > 2) {
         if (t.dim() != n - 2) Py_RETURN_NONE;
         for (Py_ssize_t i = 2; i < n; ++i) {

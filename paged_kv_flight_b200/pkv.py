@@ -521,36 +521,55 @@ def _entry(name):
     return f if _call.__module__ == __name__ else C.cast(f, _V).value
 
 
+def _here(x, name):
+    """A call runs on the current device: a tensor elsewhere raises.  Returns
+    what _pointer's kinds add to ask the same of the other tensors."""
+    d = x.get_device()
+    if d < 0 or _cur_device is None:
+        return 0
+    if d != _cur_device():
+        raise ValueError(f"{name}: on cuda:{d}, the current device is cuda:{_cur_device()}")
+    return 4 * d + 4
+
+
+def _ptr_here(x, kinds, name):
+    """_ptr, of a tensor on the current device (raw pointers pass)."""
+    if isinstance(x, torch.Tensor):
+        _here(x, name)
+    return _ptr(x, kinds, name)
+
+
 def _vec(x, n, name):
     """Device pointer of an int32 vector of n entries; raises what is wrong
     with it.  (The calls below ask _pointer first, which is quick and says
     nothing of the reason: those of a small step are bound by the host.)"""
     _rows(x, (n,), name)
-    return _ptr(x, _I32, name)
+    return _ptr_here(x, _I32, name)
 
 
 def _mat(x, shape, name):
     """The same of an int32 tensor of the given shape."""
     _rows(x, shape, name)
-    return _ptr(x, _I32, name)
+    return _ptr_here(x, _I32, name)
 
 
 def _act(x, shape, name):
     """The same of a bf16 tensor of the given shape."""
     _rows(x, shape, name)
-    return _ptr(x, _ACT, name)
+    return _ptr_here(x, _ACT, name)
 
 
 _K_I32, _K_BF16, _K_POOL, _K_F32 = range(4)       # element kinds of _pointer
 _slot_map, _rope_axes, _attn_tree, _commit = (_entry(f) for f in EXPORTS[-4:])
 
 
-def _pools(k_pool, v_pool, k_scale, v_scale):
-    """_kv, quicker."""
-    return (_pointer(k_pool, _K_POOL) or _ptr(k_pool, _POOL, "k_pool"),
-            _pointer(v_pool, _K_POOL) or _ptr(v_pool, _POOL, "v_pool"),
-            None if k_scale is None else _pointer(k_scale, _K_F32) or _ptr(k_scale, _F32, "k_scale"),
-            None if v_scale is None else _pointer(v_scale, _K_F32) or _ptr(v_scale, _F32, "v_scale"))
+def _pools(here, k_pool, v_pool, k_scale, v_scale):
+    """_kv, quicker, of tensors on the device that `here` names."""
+    pool, f32 = here + _K_POOL, here + _K_F32
+    return (_pointer(k_pool, pool) or _ptr_here(k_pool, _POOL, "k_pool"),
+            _pointer(v_pool, pool) or _ptr_here(v_pool, _POOL, "v_pool"),
+            None if k_scale is None else _pointer(k_scale, f32) or _ptr_here(k_scale, _F32, "k_scale"),
+            None if v_scale is None else _pointer(v_scale, f32) or _ptr_here(v_scale, _F32, "v_scale"))
 
 
 def _sizes(x, n, name):
@@ -560,13 +579,6 @@ def _sizes(x, n, name):
     if not isinstance(x, _Tensor) or x.dim() != n:
         raise ValueError(f"{name}: expected a tensor of {n} dimensions")
     return x.shape
-
-
-def _here(x, name):
-    """A call runs on the current device."""
-    d = x.get_device()
-    if d >= 0 and _cur_device is not None and d != _cur_device():
-        raise ValueError(f"{name}: on cuda:{d}, the current device is cuda:{_cur_device()}")
 
 
 def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, free_count, cu_q, slots, positions,
@@ -580,20 +592,19 @@ def pkv_slot_map(ctx, seq_lens, new_lens, block_tables, pages_held, free_pages, 
     n, = _sizes(slots, 1, "slots")
     cap, = _sizes(free_pages, 1, "free_pages")
     words = 0 if tree_mask is None else _sizes(tree_mask, 2, "tree_mask")[1]
-    _here(block_tables, "block_tables")
-    p = _pointer
-    st = _call(_slot_map, ctx, p(seq_lens, 0, B) or _vec(seq_lens, B, "seq_lens"),
-               p(new_lens, 0, B) or _vec(new_lens, B, "new_lens"),
-               None if parents is None else p(parents, 0, n) or _vec(parents, n, "parents"), B,
-               p(block_tables, 0, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
-               p(pages_held, 0, B) or _vec(pages_held, B, "pages_held"),
-               p(pages_out, 0, B) or _vec(pages_out, B, "pages_out"),
-               p(free_pages, 0, cap) or _vec(free_pages, cap, "free_pages"), cap,
-               p(free_count, 0, 1) or _vec(free_count, 1, "free_count"),
-               p(free_left, 0, 1) or _vec(free_left, 1, "free_left"), n, words,
-               p(cu_q, 0, B + 1) or _vec(cu_q, B + 1, "cu_q"), p(slots, 0, n) or _vec(slots, n, "slots"),
-               p(positions, 0, n) or _vec(positions, n, "positions"),
-               None if tree_mask is None else p(tree_mask, 0, n, words) or _mat(tree_mask, (n, words), "tree_mask"),
+    p, i = _pointer, _here(block_tables, "block_tables") + _K_I32
+    st = _call(_slot_map, ctx, p(seq_lens, i, B) or _vec(seq_lens, B, "seq_lens"),
+               p(new_lens, i, B) or _vec(new_lens, B, "new_lens"),
+               None if parents is None else p(parents, i, n) or _vec(parents, n, "parents"), B,
+               p(block_tables, i, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
+               p(pages_held, i, B) or _vec(pages_held, B, "pages_held"),
+               p(pages_out, i, B) or _vec(pages_out, B, "pages_out"),
+               p(free_pages, i, cap) or _vec(free_pages, cap, "free_pages"), cap,
+               p(free_count, i, 1) or _vec(free_count, 1, "free_count"),
+               p(free_left, i, 1) or _vec(free_left, 1, "free_left"), n, words,
+               p(cu_q, i, B + 1) or _vec(cu_q, B + 1, "cu_q"), p(slots, i, n) or _vec(slots, n, "slots"),
+               p(positions, i, n) or _vec(positions, n, "positions"),
+               None if tree_mask is None else p(tree_mask, i, n, words) or _mat(tree_mask, (n, words), "tree_mask"),
                _stream(stream))
     return _done(st, "pkv_slot_map", check)
 
@@ -608,15 +619,15 @@ def pkv_rope_append_axes(ctx, q, k_new, v_new, positions, sections, slots, q_out
     n, axes = q_shape[0], len(sections)
     if k_shape[0] != n or k_shape[2] != q_shape[2]:
         raise ValueError(f"k_new: shape {tuple(k_shape)} next to q of {tuple(q_shape)}")
-    _here(q, "q")
-    p, h, hk, d = _pointer, q_shape[1], k_shape[1], q_shape[2]
+    here = _here(q, "q")
+    p, i, b, h, hk, d = _pointer, here + _K_I32, here + _K_BF16, q_shape[1], k_shape[1], q_shape[2]
     sec = (_I * axes)(*sections)
-    st = _call(_rope_axes, ctx, p(q, 1, n, h, d) or _act(q, q_shape, "q"),
-               p(k_new, 1, n, hk, d) or _act(k_new, k_shape, "k_new"),
-               p(v_new, 1, n, hk, d) or _act(v_new, k_shape, "v_new"), n,
-               p(positions, 0, axes, n) or _mat(positions, (axes, n), "positions"), axes, C.addressof(sec),
-               1 if interleaved else 0, p(slots, 0, n) or _vec(slots, n, "slots"),
-               p(q_out, 1, n, h, d) or _act(q_out, q_shape, "q_out"), *_pools(k_pool, v_pool, k_scale, v_scale),
+    st = _call(_rope_axes, ctx, p(q, b, n, h, d) or _act(q, q_shape, "q"),
+               p(k_new, b, n, hk, d) or _act(k_new, k_shape, "k_new"),
+               p(v_new, b, n, hk, d) or _act(v_new, k_shape, "v_new"), n,
+               p(positions, i, axes, n) or _mat(positions, (axes, n), "positions"), axes, C.addressof(sec),
+               1 if interleaved else 0, p(slots, i, n) or _vec(slots, n, "slots"),
+               p(q_out, b, n, h, d) or _act(q_out, q_shape, "q_out"), *_pools(here, k_pool, v_pool, k_scale, v_scale),
                _stream(stream))
     return _done(st, "pkv_rope_append_axes", check)
 
@@ -630,13 +641,14 @@ def pkv_decode_attn_tree(ctx, q, k_pool, v_pool, k_scale, v_scale, block_tables,
     B, stride = _sizes(block_tables, 2, "block_tables")
     words = _sizes(tree_mask, 2, "tree_mask")[1]
     n = q_shape[0]
-    _here(q, "q")
-    p, h, d = _pointer, q_shape[1], q_shape[2]
-    st = _call(_attn_tree, ctx, p(q, 1, n, h, d) or _act(q, q_shape, "q"), *_pools(k_pool, v_pool, k_scale, v_scale),
-               p(block_tables, 0, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
-               p(seq_lens, 0, B) or _vec(seq_lens, B, "seq_lens"), p(cu_q, 0, B + 1) or _vec(cu_q, B + 1, "cu_q"),
-               p(tree_mask, 0, n, words) or _mat(tree_mask, (n, words), "tree_mask"), words, B, n,
-               p(out, 1, n, h, d) or _act(out, q_shape, "out"), _stream(stream))
+    here = _here(q, "q")
+    p, i, b, h, d = _pointer, here + _K_I32, here + _K_BF16, q_shape[1], q_shape[2]
+    st = _call(_attn_tree, ctx, p(q, b, n, h, d) or _act(q, q_shape, "q"),
+               *_pools(here, k_pool, v_pool, k_scale, v_scale),
+               p(block_tables, i, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
+               p(seq_lens, i, B) or _vec(seq_lens, B, "seq_lens"), p(cu_q, i, B + 1) or _vec(cu_q, B + 1, "cu_q"),
+               p(tree_mask, i, n, words) or _mat(tree_mask, (n, words), "tree_mask"), words, B, n,
+               p(out, b, n, h, d) or _act(out, q_shape, "out"), _stream(stream))
     return _done(st, "pkv_decode_attn_tree", check)
 
 
@@ -646,12 +658,12 @@ def pkv_tree_commit(ctx, k_pool, v_pool, k_scale, v_scale, block_tables, seq_len
     new tokens of request b in rising order; lens_out [batch] may be seq_lens."""
     B, stride = _sizes(block_tables, 2, "block_tables")
     depth = _sizes(path, 2, "path")[1]
-    _here(block_tables, "block_tables")
-    p = _pointer
-    st = _call(_commit, ctx, *_pools(k_pool, v_pool, k_scale, v_scale),
-               p(block_tables, 0, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
-               p(seq_lens, 0, B) or _vec(seq_lens, B, "seq_lens"),
-               p(path, 0, B, depth) or _mat(path, (B, depth), "path"), depth,
-               p(path_lens, 0, B) or _vec(path_lens, B, "path_lens"), B,
-               p(lens_out, 0, B) or _vec(lens_out, B, "lens_out"), _stream(stream))
+    here = _here(block_tables, "block_tables")
+    p, i = _pointer, here + _K_I32
+    st = _call(_commit, ctx, *_pools(here, k_pool, v_pool, k_scale, v_scale),
+               p(block_tables, i, B, stride) or _mat(block_tables, (B, stride), "block_tables"), stride,
+               p(seq_lens, i, B) or _vec(seq_lens, B, "seq_lens"),
+               p(path, i, B, depth) or _mat(path, (B, depth), "path"), depth,
+               p(path_lens, i, B) or _vec(path_lens, B, "path_lens"), B,
+               p(lens_out, i, B) or _vec(lens_out, B, "lens_out"), _stream(stream))
     return _done(st, "pkv_tree_commit", check)

@@ -1136,3 +1136,11 @@ def test_rope_append_axes_stores_what_the_other_appends_store(pkv, Hq, Hkv, d, P
         for got in (b[i], c[i]):
             diff = int((got.view(torch.uint8) != want).sum())
             assert diff == 0, (name, diff, want.numel())
+
+
+def test_marshal_pointers_of_one_device(pkv):
+    m = pytest.importorskip("paged_kv_flight_b200._marshal")
+    x = torch.zeros(4, 6, dtype=torch.int32, device=DEV)
+    at = x.get_device()
+    assert m.pointer(x, 4 * at + 4, 4, 6) == m.pointer(x, 0, 4, 6) == x.data_ptr()
+    assert m.pointer(x, 4 * at + 8, 4, 6) is None and m.pointer(x, 4 * at + 5, 4, 6) is None

@@ -254,3 +254,44 @@ assert got == want, got
     env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
     r = subprocess.run([sys.executable, "-c", code], cwd=root, env=env, capture_output=True, text=True)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_binding_wants_every_tensor_on_the_current_device(pkv):
+    """Not the first one alone: a length vector or a pool on another GPU is
+    refused by name, before the library is called."""
+    class _Here(torch.Tensor):
+        is_cuda = True
+
+        def get_device(self):
+            return 0
+
+    class _Elsewhere(_Here):
+        def get_device(self):
+            return 1
+
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32)   # noqa: E731
+    h = lambda *s: torch.zeros(*s, dtype=torch.bfloat16)   # noqa: E731
+    f = lambda *s: torch.zeros(*s)   # noqa: E731
+    pools = dict(k_pool=h(9, 8, 16, 128), v_pool=h(9, 8, 16, 128), k_scale=f(9, 8), v_scale=f(9, 8))
+    calls = {
+        pkv.pkv_slot_map: dict(seq_lens=i(2), new_lens=i(2), block_tables=i(2, 4), pages_held=i(2), free_pages=i(9),
+                               free_count=i(1), cu_q=i(3), slots=i(5), positions=i(5), pages_out=i(2), free_left=i(1),
+                               parents=i(5), tree_mask=i(5, 1)),
+        pkv.pkv_rope_append_axes: dict(q=h(2, 32, 128), k_new=h(2, 8, 128), v_new=h(2, 8, 128), positions=i(1, 2),
+                                       sections=[64], slots=i(2), q_out=h(2, 32, 128), **pools),
+        pkv.pkv_decode_attn_tree: dict(q=h(5, 32, 128), **pools, block_tables=i(2, 4), seq_lens=i(2), cu_q=i(3),
+                                       tree_mask=i(5, 1), out=h(5, 32, 128)),
+        pkv.pkv_tree_commit: dict(**pools, block_tables=i(2, 4), seq_lens=i(2), path=i(2, 3), path_lens=i(2),
+                                  lens_out=i(2)),
+    }
+    keep, pkv._cur_device = pkv._cur_device, lambda: 0
+    try:
+        for call, args in calls.items():
+            here = {k: v.as_subclass(_Here) if isinstance(v, torch.Tensor) else v for k, v in args.items()}
+            assert call(None, **here, stream=0, check=False) == pkv.PKV_ERR_INVALID_ARG      # NULL context, all else taken
+            for k, v in args.items():
+                if isinstance(v, torch.Tensor):
+                    with pytest.raises(ValueError, match=f"{k}: on cuda:1, the current device is cuda:0"):
+                        call(None, **dict(here, **{k: v.as_subclass(_Elsewhere)}), stream=0)
+    finally:
+        pkv._cur_device = keep
