@@ -37,26 +37,51 @@ def needs_build() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def marshal_stamp() -> str:
+    """What a built module depends on besides its source: it has torch's and
+    CPython's layouts compiled in."""
+    import torch
+
+    return f"torch {torch.__version__}, abi {int(torch._C._GLIBCXX_USE_CXX11_ABI)}, {sysconfig.get_config_var('SOABI')}"
+
+
+def marshal_current(stamp: str) -> bool:
+    if not os.path.exists(MARSHAL) or os.path.getmtime(MARSHAL) < os.path.getmtime(MARSHAL_SRC):
+        return False
+    with open(MARSHAL, "rb") as f:
+        return b"\0" + stamp.encode() + b"\0" in f.read()
+
+
 def build_marshal(force: bool = False, verbose: bool = False) -> str:
     """The binding's extension module, against the installed torch's headers.
     pkv.py does its work in Python where it is missing, so that a host without
-    a C++ compiler or those headers still has the library."""
-    if not force and os.path.exists(MARSHAL) and os.path.getmtime(MARSHAL) >= os.path.getmtime(MARSHAL_SRC):
-        return MARSHAL
-    import torch
-
-    base = os.path.dirname(torch.__file__)
-    inc = os.path.join(base, "include")
-    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-isystem", inc, "-isystem",
-           os.path.join(inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-o", MARSHAL,
-           MARSHAL_SRC, "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
-    if verbose:
-        print(" ".join(cmd))
+    a C++ compiler or those headers still has the library; a module that could
+    not be built again is removed."""
     try:
-        subprocess.run(cmd, check=True)
-    except (OSError, subprocess.CalledProcessError) as e:
+        import torch
+
+        stamp = marshal_stamp()
+        if not force and marshal_current(stamp):
+            return MARSHAL
+        base = os.path.dirname(torch.__file__)
+        inc, new = os.path.join(base, "include"), f"{MARSHAL}.{os.getpid()}.so"
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DPKV_STAMP="{stamp}"', "-isystem",
+               inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-I",
+               sysconfig.get_paths()["include"], "-o", new, MARSHAL_SRC, "-L", os.path.join(base, "lib"),
+               "-ltorch_python", "-ltorch_cpu", "-lc10"]
+        if verbose:
+            print(" ".join(cmd))
+        try:
+            subprocess.run(cmd, check=True)
+            os.replace(new, MARSHAL)
+        finally:
+            if os.path.exists(new):
+                os.remove(new)
+    except (ImportError, OSError, subprocess.CalledProcessError) as e:
         print(f"_marshal.so not built ({e}): the binding's checks stay in Python", file=sys.stderr)
+        if os.path.exists(MARSHAL):
+            os.remove(MARSHAL)
     return MARSHAL
 
 

@@ -80,4 +80,18 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// What this was built against (build.py compares it before it keeps the file,
+// pkv.py before it uses the module).
+#ifndef PKV_STAMP
+#error "PKV_STAMP: the versions of torch and Python, from build.py"
+#endif
+
+PyMODINIT_FUNC PyInit__marshal()
+{
+    PyObject* m = PyModule_Create(&module);
+    if (m && PyModule_AddStringConstant(m, "built_for", PKV_STAMP) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}

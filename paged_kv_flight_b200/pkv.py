@@ -503,16 +503,18 @@ def _rows(x, shape, name):
 
 _Tensor = torch.Tensor
 try:
-    from . import _marshal
+    from . import _marshal, build as _build
+    if getattr(_marshal, "built_for", None) != _build.marshal_stamp():
+        raise ImportError("_marshal was built against another torch or Python")
     _pointer, _call = _marshal.pointer, _marshal.call
-except ImportError:                      # not built: the same checks, in Python alone
+except ImportError:                      # not built, or not for this torch: the same checks, in Python alone
     def _pointer(*_):
         return None
 
     def _call(function, *args):
         return function(*args)
 else:
-    del _marshal
+    del _marshal, _build
 
 
 def _entry(name):

@@ -295,3 +295,33 @@ def test_binding_wants_every_tensor_on_the_current_device(pkv):
                         call(None, **dict(here, **{k: v.as_subclass(_Elsewhere)}), stream=0)
     finally:
         pkv._cur_device = keep
+
+
+def test_marshal_module_of_another_torch(pkv, tmp_path, monkeypatch):
+    """A module built against other headers is not current, one that cannot be
+    built again does not stay, and the binding uses none but its own torch's."""
+    import os
+    import subprocess
+    import sys
+
+    from paged_kv_flight_b200 import build
+    stamp = build.marshal_stamp()
+    assert torch.__version__ in stamp
+    if os.path.exists(build.MARSHAL):
+        assert build.marshal_current(stamp) and not build.marshal_current(stamp.replace("torch ", "torch 9"))
+    old = tmp_path / "_marshal.so"
+    old.write_bytes(b"\0torch 1.0, abi 1, cpython-30\0")
+    monkeypatch.setattr(build, "MARSHAL", str(old))
+    monkeypatch.setenv("CXX", "false")
+    assert not build.marshal_current(stamp)
+    build.build_marshal()
+    assert not old.exists() and not list(tmp_path.iterdir())
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    code = """
+from paged_kv_flight_b200 import build
+build.marshal_stamp = lambda: 'torch 9'
+from paged_kv_flight_b200 import pkv
+assert pkv._pointer.__module__ == pkv._call.__module__ == pkv.__name__
+"""
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr[-2000:]
