@@ -209,16 +209,16 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
     const size_t rows_units = std::max(units * ctx->G, (size_t)ctx->attn.ctas * pkv::kAttnWarps * pkv::kMaxTokenRows);
     const size_t b_err = 256;
     const size_t b_cnt = ((size_t)(std::max(cfg->max_batch, ctx->vmax) + 8) * sizeof(int) + 255) & ~(size_t)255;
-    const size_t b_po = 2 * rows_units * cfg->head_dim * sizeof(float);
-    const size_t b_pml = 2 * rows_units * 2 * sizeof(float);
+    // The tree attention's parts, two of 256 rows per CTA, lie in the same place: what
+    // a call leaves there nobody reads, and the calls of a context follow one another
+    ctx->tree_runs = std::min(ctx->num_sms, pkv::kMaxTreeRuns);
+    const size_t rows = std::max(2 * rows_units, 2 * (size_t)ctx->tree_runs * 2 * pkv::kTreeRows);
+    const size_t b_po = rows * cfg->head_dim * sizeof(float);
+    const size_t b_pml = rows * 2 * sizeof(float);
     const size_t b_vm = 2 * ((size_t)ctx->vmax * sizeof(int4) + 256);   // varlen plans (virtual, chunk) + counts
     const size_t b_th = ((size_t)cfg->head_dim / 2 * sizeof(double) + 255) & ~(size_t)255;   // RoPE frequencies
-    // the tree attention: two parts of 256 rows per CTA, and where the CTAs start
-    ctx->tree_runs = std::min(ctx->num_sms, pkv::kMaxTreeRuns);
-    const size_t t_rows = 2 * (size_t)ctx->tree_runs * 2 * pkv::kTreeRows;
-    const size_t b_to = t_rows * cfg->head_dim * sizeof(float), b_tml = t_rows * sizeof(float2);
-    const size_t b_tp = ((size_t)(ctx->tree_runs + 1) * sizeof(int4) + 255) & ~(size_t)255;
-    ctx->ws_bytes = b_err + b_cnt + b_po + b_pml + b_vm + b_th + b_to + b_tml + b_tp;
+    const size_t b_tp = ((size_t)(ctx->tree_runs + 1) * sizeof(int4) + 255) & ~(size_t)255;   // where the tree attention's CTAs start
+    ctx->ws_bytes = b_err + b_cnt + b_po + b_pml + b_vm + b_th + b_tp;
     if (cudaMalloc(&ctx->ws, ctx->ws_bytes) != cudaSuccess) {
         cudaGetLastError();
         free(ctx);
@@ -237,9 +237,9 @@ pkv_status pkv_create(const pkv_config* cfg, pkv_ctx** out)
     ctx->d_cmap = reinterpret_cast<int4*>(base + b_err + b_cnt + b_po + b_pml + b_vm / 2 + 256);
     ctx->prefill_rows = pkv::kDefaultPrefillRows;
     ctx->d_theta = reinterpret_cast<double*>(base + b_err + b_cnt + b_po + b_pml + b_vm);
-    ctx->d_tree_o = reinterpret_cast<float*>(reinterpret_cast<uint8_t*>(ctx->d_theta) + b_th);
-    ctx->d_tree_ml = reinterpret_cast<float2*>(reinterpret_cast<uint8_t*>(ctx->d_tree_o) + b_to);
-    ctx->d_tree_pos = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctx->d_tree_ml) + b_tml);
+    ctx->d_tree_o = ctx->d_part_o;
+    ctx->d_tree_ml = reinterpret_cast<float2*>(ctx->d_part_ml);
+    ctx->d_tree_pos = reinterpret_cast<int4*>(reinterpret_cast<uint8_t*>(ctx->d_theta) + b_th);
     // theta_i = rope_base^(-2i/d) once, in fp64 on the host
     double theta[64];
     for (int i = 0; i < cfg->head_dim / 2; ++i) theta[i] = pow(cfg->rope_base, (-2.0 * i) / cfg->head_dim);

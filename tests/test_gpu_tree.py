@@ -1144,3 +1144,37 @@ def test_marshal_pointers_of_one_device(pkv):
     at = x.get_device()
     assert m.pointer(x, 4 * at + 4, 4, 6) == m.pointer(x, 0, 4, 6) == x.data_ptr()
     assert m.pointer(x, 4 * at + 8, 4, 6) is None and m.pointer(x, 4 * at + 5, 4, 6) is None
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(8, 8, 64), (8, 2, 64), (32, 8, 128), (64, 8, 128)])
+def test_workspace_is_shared_between_the_calls(pkv, Hq, Hkv, d):
+    """The tree attention's parts lie where the other attentions keep theirs: a
+    context holds what the largest of them needs, and calls of every kind in turn
+    on one stream give what each gives alone."""
+    lens = [3000, 90, 1500, 7]
+    n = 16 // (Hq // Hkv) // 2
+    x = _attn_inputs((Hq, Hkv, d, 16, False, lens, [n] * 4, "chain"))
+    g = _attn_device(x)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    q4 = g["q"].view(4, n, Hq, d)
+    with _attn_ctx(pkv, x, batch=64) as ctx:
+        # rows: 2 parts of 9 units of 8 warps of G rows, or of 256 of the tree attention, an SM
+        rows = sms * max(2 * 9 * 8 * (Hq // Hkv), 2 * 256)
+        assert pkv.pkv_workspace_bytes(ctx) <= rows * (d + 2) * 4 + (1 << 18)
+
+        def calls():
+            o = [torch.empty_like(g["q"]) for _ in range(3)] + [torch.empty_like(q4[:, 0])]
+            pkv.pkv_decode_attn_tree(ctx, g["q"], g["k"], g["v"], None, None, g["table"], g["lens"], g["cu"], g["mask"], o[0])
+            pkv.pkv_decode_attn_tokens(ctx, q4, g["k"], g["v"], None, None, g["table"], g["lens"], o[1].view(q4.shape))
+            pkv.pkv_decode_attn_varlen(ctx, g["q"], g["k"], g["v"], None, None, g["table"], g["lens"], g["cu"], o[2])
+            pkv.pkv_decode_attn(ctx, q4[:, 0].contiguous(), g["k"], g["v"], None, None, g["table"], g["lens"], o[3])
+            return o
+
+        alone = calls()
+        torch.cuda.synchronize()
+        rounds = [calls() for _ in range(30)]
+        torch.cuda.synchronize()
+        _ok(pkv, ctx)
+        _attn_near(alone[0], *_attn_ref(x))
+        for o in rounds:
+            assert all(torch.equal(a, b) for a, b in zip(o, alone))
