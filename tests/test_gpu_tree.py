@@ -1178,3 +1178,76 @@ def test_workspace_is_shared_between_the_calls(pkv, Hq, Hkv, d):
         _attn_near(alone[0], *_attn_ref(x))
         for o in rounds:
             assert all(torch.equal(a, b) for a, b in zip(o, alone))
+
+
+@pytest.mark.parametrize("B,hi,t_hi,tree", [(1500, 40, 3, True), (8192, 40, 3, False), (900, 30, 60, True)])
+@pytest.mark.parametrize("inplace", [False, True])
+def test_slot_map_large(pkv, B, hi, t_hi, tree, inplace):
+    """More requests than threads, more rows than the cluster takes at once."""
+    rng = np.random.default_rng(B)
+    x = _slot_inputs(rng, B, 16, 0, hi, 0, t_hi, tree)
+    cap, words = int(x["new"].sum()) + 7, 2
+    r = _tree.slot_map(x["lens"], x["new"], x["table"], x["held"], x["free"], x["count"], 16, cap, x["parents"], words)
+    with _Ctx(pkv, 8, 2, 64, 16, False, B, x["table"].shape[1], x["pages"]) as ctx:
+        _slot_check(_slot_call(pkv, ctx, x, cap, words, inplace), r)
+        _ok(pkv, ctx)
+
+
+def test_slot_map_one_large_tree(pkv):
+    """Ancestors further back than the rows that a CTA holds."""
+    rng = np.random.default_rng(4)
+    n, L, P = 3000, 21, 32
+    par = _tree.parents_of(rng, n)
+    par[2900:] = [i % 50 for i in range(100)]
+    seen = _tree.ancestors(par)
+    table, pages, _ = _tree.tables(rng, [-(-(L + n) // P)])
+    x = dict(lens=np.array([L]), new=np.array([n]), held=np.array([table.shape[1]]), table=table, free=np.array([0]),
+             count=0, parents=np.array(par, np.int32))
+    words = -(-n // 32)
+    r = _tree.slot_map(x["lens"], x["new"], table, x["held"], x["free"], 0, P, n)
+    r["pos"], r["mask"] = (L + seen.sum(1) - 1).astype(np.int32), _tree.pack(seen, words)
+    with _Ctx(pkv, 8, 2, 64, P, False, 1, table.shape[1], pages) as ctx:
+        _slot_check(_slot_call(pkv, ctx, x, n, words), r)
+        _ok(pkv, ctx)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_tree_attention_more_requests_than_threads(pkv, fp8):
+    rng = np.random.default_rng(12)
+    lens = [int(v) for v in rng.integers(0, 40, 600)]
+    new = [int(v) for v in rng.integers(0, 4, 600)]
+    x = _attn_inputs((4, 2, 64, 16, fp8, lens, new, "random"))
+    ref, size = _attn_ref(x)
+    with _attn_ctx(pkv, x) as ctx:
+        out = _attn_run(pkv, ctx, _attn_device(x))
+        _ok(pkv, ctx)
+        _attn_near(out, ref, size)
+
+
+@pytest.mark.parametrize("Hkv,depth,fp8", [(2, 300, False), (2, 300, True), (72, 9, False), (72, 9, True), (40, 4, True)])
+def test_tree_commit_large(pkv, Hkv, depth, fp8):
+    """Paths longer than the places kept in shared memory, more kv heads than a
+    cluster takes at once."""
+    test_tree_commit(pkv, Hkv, Hkv, 64, 16, fp8, 3, depth, True)
+
+
+def test_calls_on_another_device_than_the_contexts(pkv):
+    """A context of another GPU is refused before anything is launched (made up:
+    the checks read its configuration, then its device)."""
+    import ctypes as C
+    blob = C.create_string_buffer(b"\x07" * (1 << 16), 1 << 16)
+    cfg = pkv.make_config(8, 2, 64, 16, "bf16", 1e4, 8, 8, 20)
+    C.memmove(blob, C.byref(cfg), C.sizeof(cfg))
+    ctx = C.addressof(blob)
+    i = lambda *s: torch.zeros(*s, dtype=torch.int32, device=DEV)   # noqa: E731
+    h = lambda *s: torch.zeros(*s, dtype=torch.bfloat16, device=DEV)   # noqa: E731
+    pool = h(20, 2, 16, 64)
+    calls = [lambda: pkv.pkv_slot_map(ctx, i(2), i(2), i(2, 8), i(2), i(9), i(1), i(3), i(5), i(5), i(2), i(1), check=False),
+             lambda: pkv.pkv_rope_append_axes(ctx, h(2, 8, 64), h(2, 2, 64), h(2, 2, 64), i(1, 2), [32], i(2), h(2, 8, 64),
+                                              pool, pool.clone(), None, None, check=False),
+             lambda: pkv.pkv_decode_attn_tree(ctx, h(5, 8, 64), pool, pool, None, None, i(2, 8), i(2), i(3), i(5, 1),
+                                              h(5, 8, 64), check=False),
+             lambda: pkv.pkv_tree_commit(ctx, pool, pool, None, None, i(2, 8), i(2), i(2, 3), i(2), i(2), check=False)]
+    for call in calls:
+        assert call() == pkv.PKV_ERR_INVALID_ARG
+    torch.cuda.synchronize()
