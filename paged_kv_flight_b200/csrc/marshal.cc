@@ -8,6 +8,8 @@
 #include <Python.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <exception>
+
 namespace {
 
 // pointer(x, kind, size, ...): the device address of a contiguous CUDA tensor
@@ -15,7 +17,7 @@ namespace {
 // or None: then the caller looks closer.
 // kind 0: int32, 1: bf16, 2: a pool (bf16, uint8 or E4M3 codes), 3: float32; plus
 // 4 (g + 1) where only tensors on cuda:g will do.
-PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t n)
+PyObject* pointer_of(PyObject* const* args, Py_ssize_t n)
 {
     if (n < 2) {
         PyErr_SetString(PyExc_TypeError, "pointer(x, kind, sizes...)");
@@ -41,6 +43,17 @@ PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t n)
         }
     }
     return PyLong_FromUnsignedLongLong(reinterpret_cast<unsigned long long>(t.data_ptr()));
+}
+
+// Tensors without storage (inside torch.func's transforms) throw when asked for
+// their address: an exception must not pass through the interpreter.
+PyObject* pointer(PyObject*, PyObject* const* args, Py_ssize_t n)
+{
+    try {
+        return pointer_of(args, n);
+    } catch (const std::exception&) {
+        Py_RETURN_NONE;
+    }
 }
 
 // call(address, a, ...): the C function at the address with up to 20 integers

@@ -1251,3 +1251,20 @@ def test_calls_on_another_device_than_the_contexts(pkv):
     for call in calls:
         assert call() == pkv.PKV_ERR_INVALID_ARG
     torch.cuda.synchronize()
+
+
+def test_marshal_of_tensors_without_storage(pkv):
+    """A tensor that has no address (inside a transform of torch.func) raises; it
+    used to end the process."""
+    m = pytest.importorskip("paged_kv_flight_b200._marshal")
+    seen = []
+
+    def inside(x):
+        assert type(x) is torch.Tensor
+        seen.append(m.pointer(x, 0))
+        with pytest.raises(RuntimeError):
+            pkv.pkv_tree_commit(None, 0, 0, None, None, x, 0, torch.zeros(4, 2, dtype=torch.int32, device=DEV), 0, 0)
+        return x
+
+    torch.func.vmap(inside)(torch.zeros(3, 4, 5, dtype=torch.int32, device=DEV))
+    assert seen == [None]
