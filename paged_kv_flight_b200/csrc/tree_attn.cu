@@ -322,6 +322,8 @@ __device__ __forceinline__ constexpr uint32_t p_col(int kk)
     return (uint32_t)(16 * kk / N * N + 16 * kk % N / 2);
 }
 
+constexpr float kOneUp = 1.f + 1.f / (1 << 23);
+
 // One pass over the row's S, 64 keys (E4M3: 32) at a time in a loop that is not unrolled
 // (unrolled, the code was over 64 KB, and fetching it made every warp of the SM
 // several times slower).  A chunk's maximum is taken
@@ -333,7 +335,9 @@ __device__ __forceinline__ constexpr uint32_t p_col(int kk)
 // hold the first terms, keys 2i and 2i + 1 in column i, the others the second.
 // The first term is the weight's upper half, cut (no conversion, and the rest,
 // below 2^-7 of the weight, is an exact difference); the second is the rest rounded.
-// l is summed from the fp32 weights, of which the two terms leave 2^-15 at most.
+// It is made larger by 2^-23 of the weight, so that it is 0 for no weight but 0: next
+// to an infinity in V a second term of 0 would make NaN of it.  l is summed from the
+// fp32 weights, of which the two terms leave 2^-15 at most.
 //
 // f: score scale in log2 units.  E4M3: `scales` of lane k holds the K scale of
 // the tile's page k, of lane 8 + k its V scale; pages are 1 << shift keys.
@@ -403,8 +407,8 @@ __device__ __forceinline__ void tile_softmax(uint32_t scol, uint32_t ocol, bool 
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int c = 16 * h + 2 * i;
-                const float r0 = __uint_as_float(x[c]) - __uint_as_float(x[c] & 0xFFFF0000u),
-                            r1 = __uint_as_float(x[c + 1]) - __uint_as_float(x[c + 1] & 0xFFFF0000u);
+                const float r0 = fmaf(__uint_as_float(x[c]), kOneUp, -__uint_as_float(x[c] & 0xFFFF0000u)),
+                            r1 = fmaf(__uint_as_float(x[c + 1]), kOneUp, -__uint_as_float(x[c + 1] & 0xFFFF0000u));
                 w[i] = pack_bf16(r0, r1);
             }
             tmem_st8(scol + (uint32_t)(N * k + N / 2 + 8 * h), w);

@@ -1268,3 +1268,24 @@ def test_marshal_of_tensors_without_storage(pkv):
 
     torch.func.vmap(inside)(torch.zeros(3, 4, 5, dtype=torch.int32, device=DEV))
     assert seen == [None]
+
+
+@pytest.mark.parametrize("zero_q", [False, True])
+@pytest.mark.parametrize("L", [200, 6000])
+def test_tree_attention_infinite_cached_values(pkv, zero_q, L):
+    """An infinity in V of a cached key is an infinity of its sign in that column
+    of every row, also where weights are exact in bf16 (q = 0: all of them 1), and
+    nothing anywhere else."""
+    x = _attn_inputs((8, 2, 128, 16, False, [L, 9], [5, 3], "random"))
+    if zero_q:
+        x["q"].zero_()
+    ref, size = _attn_ref(x)
+    for pos, col, v in ((30, 7, float("inf")), (L - 50, 9, -float("inf"))):
+        x["v"][x["table"][0, pos // 16], 0, pos % 16, col] = v
+    with _attn_ctx(pkv, x) as ctx:
+        got = _tree.values(_attn_run(pkv, ctx, _attn_device(x)))
+        _ok(pkv, ctx)
+    assert (got[:5, :4, 7] == np.inf).all() and (got[:5, :4, 9] == -np.inf).all()
+    for col in (7, 9):
+        got[:5, :4, col] = ref[:5, :4, col]
+    assert (np.abs(got - ref) <= 2.0 ** -8 * np.abs(ref) + W * size).all()
