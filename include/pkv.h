@@ -331,19 +331,22 @@ pkv_status pkv_table_sync(const int32_t* upload, int n_changes, int batch, int m
  * Apart from the two pairs named, no output may overlap an input.  All
  * pointers 4-byte aligned.  batch == 0 is a no-op.
  *
- * Device-side errors, each sticky in the error word: a request whose pages
- * the stack cannot cover keeps pages_held, its tokens get slot -1 and no page
- * is taken for it (PKV_ERR_OOM; requests before it, and later ones that need
- * no page, are served), and the table entries of the pages it lacks become -1, so
- * that the attention leaves their keys out and pkv_tree_commit refuses a path
- * through them (its tokens are not stored anywhere: the path to give it is empty;
- * the same for a request with more tokens than its table or mask_words hold); a length, count or held value out of range, more
- * drafted tokens than 32 mask_words, or a parent that is not an earlier token
- * (slot -1, PKV_ERR_DEVICE_BOUNDS); a table or stack entry that is no page
- * (the slots in it -1); more tokens than n_tokens (the surplus has no
- * row and cu_q is clipped; the pages are taken and entered for all tokens, so
- * that block_tables, pages_out and free_left agree and a next step can go on;
- * PKV_ERR_DEVICE_BOUNDS.  A count out of range takes the rows behind it so). */
+ * Device-side errors, each sticky in the error word:
+ *   a request whose pages the stack cannot cover keeps pages_held, its tokens
+ *       get slot -1 and no page is taken for it (PKV_ERR_OOM; requests before it,
+ *       and later ones that need no page, are served); the table entries of the
+ *       pages it lacks become -1, so that the attention leaves their keys out and
+ *       pkv_tree_commit refuses a path through them (its tokens are not stored:
+ *       the path to give it is empty);
+ *   a length, count or held value out of range, more drafted tokens than 32
+ *       mask_words, or a parent that is not an earlier token (slot -1,
+ *       PKV_ERR_DEVICE_BOUNDS); a request with more tokens than its table or
+ *       mask_words hold gets entries of -1 like the one above;
+ *   a table or stack entry that is no page (the slots in it -1);
+ *   more tokens than n_tokens: the surplus has no row and cu_q is clipped
+ *       (PKV_ERR_DEVICE_BOUNDS); pages are taken and entered for all tokens, so
+ *       that block_tables, pages_out and free_left agree and a next step can go
+ *       on.  A count out of range takes the rows behind it so. */
 pkv_status pkv_slot_map(pkv_ctx* ctx, const int32_t* seq_lens, const int32_t* new_lens, const int32_t* parents,
                         int batch, int32_t* block_tables, int bt_stride, const int32_t* pages_held,
                         int32_t* pages_out, const int32_t* free_pages, int free_cap, const int32_t* free_count,
@@ -391,7 +394,8 @@ pkv_status pkv_rope_append_axes(pkv_ctx* ctx, const void* q, const void* k_new, 
  *   q, out     [n_tokens][Hq][d] bf16; rows outside every request are left
  *              as they were.  q and out may not overlap.
  *   tree_mask  [n_tokens][mask_words] 32-bit words, T_b <= 32 mask_words
- * bf16 or E4M3 pools (scales as for pkv_decode_attn, finite, >= 0).  The cache is read
+ * bf16 or E4M3 pools (scales as for pkv_decode_attn, finite, >= 0; finite values of V
+ * below 2^96: weights are up to 2^24 before they are divided by their sum).  The cache is read
  * once for every 2 * (128 / G) new tokens of a request.  Weights keep 2^-15 of
  * themselves in the product with V (two bf16 terms), sums are fp32.  What K and V
  * of new tokens hold that a row does not see, NaN and infinity included, does not

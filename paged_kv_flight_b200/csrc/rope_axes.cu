@@ -28,12 +28,12 @@ namespace {
 // One CTA per token; a thread takes 8 pairs of a head at a time (two 16-byte
 // loads, neighbouring lanes side by side), the first of them ahead of the angles.
 //
-// What bounds it: for long calls memory, then the wait for the fp64 angles and the
-// instructions beside it.  Measured (B200): 8192 tokens of 64 + 8 heads of 128,
-// 62.7 us, 82% of the measured copy (57.5 in fp32 alone; 65.0 with every load behind
-// the angles; 83 with no table, the rare values taking their own fp64 angles; 72 with
-// more CTAs an SM and spilled registers).  64 tokens, 6.0 us a call among others: a
-// launch and three dependent loads.
+// What bounds it: for long calls memory and the instructions (issue slots 69% taken,
+// by ncu).  Measured (two B200s): 8192 tokens of 64 + 8 heads of 128, 59.9 and 62.7
+// us, 82 to 87% of the measured copy (57.5 in fp32 alone; on the slower one 65.0 with
+// every load behind the angles, 83 with no table, the rare values taking their own
+// fp64 angles, 93 with 12 CTAs an SM by spilling registers).  64 tokens, 6.1 us a call
+// among others: a launch and three dependent loads.
 constexpr int kAxesThreads = 128;
 
 constexpr float kDelta = 5.f / (1 << 24);

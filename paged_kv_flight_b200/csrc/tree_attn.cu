@@ -35,14 +35,15 @@
 // as many P V MMAs) each weight is off by up to 2^-8, as much again as the output's
 // own rounding, and a row that sees one key does not get its V back.
 //
-// What bounds it, and what it measured (B200, us a call): the chain of a tile, S,
-// softmax, P V and the handovers between them, of which tensor memory holds two at
-// d = 128; the second term of P lengthens it by 512 cycles.  Long caches (8 requests
-// of 32k to 128k tokens, 8 new ones each, 2.28 GB: 468, 75% of the measured copy; 396
-// with one term), serving batches (64 requests of 128 to 4096, 9 to 16 new ones, 555
-// MB: 139; 119), large trees (48 requests, 33 to 64 new tokens of 64 heads: 201, where
-// the products alone take 78; 169), E4M3 caches, beside the conversion (64 requests,
-// 391 MB: 187; 167); a few short requests, latency (4 requests: 12.2).
+// What bounds it, and what it measured (two B200s, us a call): the chain of a tile,
+// S, softmax, P V and the handovers between them, two of which are under way at a
+// time; the second term of P makes its MMAs half as many again (in brackets: with one
+// term).  Long caches (8 requests of 32k to 128k tokens, 8 new ones each, 2.28 GB: 426
+// and 460 [357 and 396], 76 to 83% of the measured copy), serving batches (64 requests
+// of 128 to 4096, 9 to 16 new ones, 555 MB: 131 and 138 [113 and 119]), large trees (48
+// requests, 33 to 64 new tokens of 64 heads: 193 and 201 [162 and 169], where the
+// products alone take 78), E4M3 caches, beside the conversion (64 requests, 391 MB: 182
+// and 185 [158 and 167]); a few short requests, latency (4 requests: 12.3 [11.8]).
 #include "tree_params.h"
 #include "pkv_device.cuh"
 #include "umma.cuh"
@@ -66,7 +67,7 @@ constexpr uint64_t kTWaitNs = 500ull * 1000ull * 1000ull;
 // took 1.5 to 2 times the mean (297 us against 184 for large trees); with 7 or 12 for
 // the item they took 3 and 2% longer.  With P in two terms a tile takes about a
 // quarter more in both modes, and 7, 8 and 9 for the item are alike within 1%, for
-// E4M3 caches too.
+// E4M3 caches too.  Heads of 64 have the same costs, not fitted for them.
 constexpr int kCostRowShift = 2, kCostKeyShift = 1, kCostItem = 9;
 constexpr int kCostRow = 1 << kCostRowShift, kCostKey = 1 << kCostKeyShift;
 // How far a row's maximum may pass its reference, in powers of two, before the
